@@ -260,8 +260,7 @@ def _pages_plain(s):
     ids = table[r, at].long()
     slots = torch.where((i < cu_rows[-1]) & (row // page < table.shape[1]) & (ids >= 0), ids * page + row % page, -1)
     taken = cu_pages[-1].clamp(max=free.numel())
-    lost = ((slots < 0) & (i < cu_rows[-1])).sum() + (cu_rows[-1] - cap).clamp(min=0)
-    counts = torch.stack([cu_rows[-1], taken, cu_pages[-1] - taken, lost]).int()
+    counts = torch.stack([cu_rows[-1], taken, cu_pages[-1] - taken, need.max()]).int()
     return {"table": table.int(), "cu_rows": cu_rows.int(), "slots": slots, "counts": counts}
 
 
