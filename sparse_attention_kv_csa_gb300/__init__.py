@@ -20,6 +20,9 @@ device addresses.  bf16 tensors may be torch.bfloat16 or any 16-bit dtype
 holding bf16 bit patterns.  ``stream`` is a torch.cuda.Stream, a raw
 cudaStream_t integer, or None for torch's current stream.
 
+The entry points of include/csa_serving.h (norm, page tables, attention over the
+rows) and their helpers are in ``serving`` and re-exported here.
+
 compress_forward / compress_backward allocate the outputs with torch and call
 the same entry points (the layout of the "CSA Fused Compressor" wrappers).
 """
@@ -28,13 +31,14 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import _build
+from . import _build, serving
+from .serving import *  # noqa: F401,F403
 
 __all__ = [
     "csa_compress_fwd", "csa_compress_bwd", "csa_compress_bwd_noalloc", "csa_check_support", "csa_status_string",
     "csa_last_error_message", "csa_version", "csa_device_status", "csa_selftest_bounded_wait",
     "csa_selftest_reciprocal", "csa_grad_ape_order", "CSAError", "compress_forward", "compress_backward",
-    "library_path", "STATUS",
+    "library_path", "STATUS", *serving.__all__,
 ]
 
 STATUS = {
@@ -105,6 +109,9 @@ def _stream(s):
 def _check(rc: int):
     if rc != 0:
         raise CSAError(rc, _lib.csa_last_error_message().decode())
+
+
+serving._bind(_lib, _check)
 
 
 def csa_status_string(status: int) -> str:

@@ -18,6 +18,7 @@
 #include "csa.h"
 #include "csa_device.cuh"
 #include "csa_launch.h"
+#include "csa_serving_launch.h"
 
 namespace {
 
@@ -212,8 +213,8 @@ struct ResidentKey {
 cudaError_t cached_resident(const ResidentKey &k, int *resident, cudaError_t (*query)(const ResidentKey &, int *))
 {
     static std::mutex mu;
-    static ResidentKey keys[64];
-    static int vals[64];
+    static ResidentKey keys[256];
+    static int vals[256];
     static int n = 0;
     {
         std::lock_guard<std::mutex> g(mu);
@@ -228,7 +229,7 @@ cudaError_t cached_resident(const ResidentKey &k, int *resident, cudaError_t (*q
     if (e != cudaSuccess)
         return e;
     std::lock_guard<std::mutex> g(mu);
-    if (n < 64) {
+    if (n < 256) {
         keys[n] = k;
         vals[n] = *resident;
         ++n;
@@ -429,6 +430,21 @@ cudaError_t launch_bwd(const BwdParams &p, const BwdPlan &b, float *partial, uns
     case kBwdStream: return launch_bwd_stream(p, b.sp, partial, status, st);
     default: return launch_bwd_small(p, b.pl, partial, st);
     }
+}
+
+cudaError_t device_facts(int *num_sms, cudaMemPool_t *pool, unsigned **status)
+{
+    DeviceState *ds = nullptr;
+    cudaError_t e = device_state(&ds);
+    if (e != cudaSuccess)
+        return e;
+    if (num_sms)
+        *num_sms = ds->num_sms;
+    if (pool)
+        *pool = ds->pool;
+    if (status)
+        *status = ds->status;
+    return cudaSuccess;
 }
 
 int fail_status(int status, const char *fmt, ...)
