@@ -1,0 +1,799 @@
+// Attention over a paged cache of shared latent rows on the tensor cores (tcgen05).
+//
+// The query rows of a request are its (token, head) pairs, in order; all of them read the same cache rows.  An item is
+// 64 such rows.  For each tile of 64 cache rows:
+//
+//   S = Q K^T          64 x 64, K = head_dim: both operands K-major in shared memory
+//   P = exp2(S f - m)  f = scale log2 e, m the row's reference; l += sum P; P to bf16 in shared memory
+//   O = O + P V        64 x v_dim, K = 64 cache rows; V is the K tile itself, read with its rows along K
+//
+// so a cache row is fetched once and used for both products.  m is raised (O and l scaled down) only when a logit
+// exceeds it by 2^8: P stays below 2^8, which bf16 and the fp32 sums hold as well as values below one, and O is
+// rarely touched outside the tensor core.
+//
+// Tensor memory: a 64-row accumulator takes 16 of each 32 lanes, so O (up to 512 columns) has the lower sixteen and
+// two S tiles the upper sixteen.  64 query rows, not 128: O of 128 x 512 alone would fill tensor memory, and a K tile
+// of 576 columns and 128 query rows would not fit shared memory twice.
+//
+// Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs, the
+// others fetch rows: global memory to registers (a tile ahead), 8-bit values widened to bf16 (exact), then to shared memory
+// in the swizzled layout.  8-bit rows carry one scale a row: it multiplies S by column and P before its rounding, so
+// it costs no precision.
+//
+// Work is cut evenly: item i counts one unit for its queries and output and one for each tile; block c takes the units
+// [c T / G, (c+1) T / G) of the T units.  Items that cross a cut leave (O, m, l) of their parts in the workspace and a
+// second kernel joins them in order.  Nothing else depends on the grid, and no order on timing.
+#include <cuda_fp8.h>
+
+#include "csa_launch.h"
+#include "csa_serving_launch.h"
+#include "csa_tcgen05.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kTile = 64;                         // query rows of an item, cache rows of a tile
+constexpr int kChunkBytes = kTile * 128;          // 64 rows x 64 bf16 columns
+constexpr int kSoftWarps = 4;
+constexpr int kMmaWarp = 4;
+constexpr int kLoadWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kMaxStages = 4;
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRaise = 8.0f;                    // log2 of how far a logit may exceed the reference
+
+struct MmaPlan {
+    int nk;           // 64-column chunks of a row
+    int stages;
+    int blocks;       // G
+    int min_units;
+    uint32_t tmem_columns;
+    size_t smem;
+    float *part_o;    // [2 blocks][64][v_dim]
+    float2 *part_ml;  // [2 blocks][64]  (m, l)
+    int4 *joins;      // [blocks]  (query row, rows, last block, valid): the item that block c is the first of several for
+};
+
+struct Shared {
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], p_full, q_full, drained;
+    long long sums[kThreads / 32];
+    long long total;
+    int r, m, off;               // where the block's units begin
+    uint32_t tmem;
+    alignas(16) float scales[kMaxStages][kTile];
+    alignas(8) uint8_t valid[kMaxStages][8], poison[kMaxStages][8];
+};
+
+// What an item is made of.
+struct Request {
+    int first;    // first token
+    int nq;
+    int before;   // tokens of the request before its first new one (may be negative)
+    int items;
+};
+
+__device__ __forceinline__ Request request(const AttnParams &p, int r)
+{
+    Request q;
+    q.first = max(__ldg(p.cu_q + r), 0);
+    const int64_t end = min((int64_t)__ldg(p.cu_q + r + 1), p.n_tokens);
+    q.nq = (int)max(end - q.first, (int64_t)0);
+    q.before = __ldg(p.seq_lens + r) - (__ldg(p.cu_q + r + 1) - q.first);
+    q.items = (int)(((int64_t)q.nq * p.n_heads + kTile - 1) / kTile);
+    return q;
+}
+
+__device__ __forceinline__ int visible(const AttnParams &p, const Request &q, int token)
+{
+    const int held = q.before + token + 1;
+    return held <= 0 ? 0 : min(held / p.ratio, p.width * p.page_size);
+}
+
+__device__ __forceinline__ int last_token(const AttnParams &p, const Request &q, int m)
+{
+    const int64_t row = min((int64_t)(m + 1) * kTile, (int64_t)q.nq * p.n_heads) - 1;
+    return (int)(row / p.n_heads);
+}
+
+__device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
+{
+    return (visible(p, q, last_token(p, q, m)) + kTile - 1) / kTile;
+}
+
+// The block's segments, walked alike by every role.
+struct Walk {
+    const AttnParams &p;
+    Request q;
+    int r, m, off;
+    long long left;
+    int nt, t0, t1;
+    __device__ Walk(const AttnParams &p_, const Shared &s, long long units) : p(p_), r(s.r), m(s.m), off(s.off), left(units)
+    {
+        if (left > 0)
+            q = request(p, r);
+    }
+    // the next segment: tiles [t0, t1) of item (r, m); nt == 0 (t0 == t1) is an item that sees nothing
+    __device__ bool next()
+    {
+        while (left > 0) {
+            while (m >= q.items) {
+                if (++r >= p.n_req)
+                    return false;
+                m = 0;
+                q = request(p, r);
+            }
+            nt = item_tiles(p, q, m);
+            const int take = (int)min((long long)(nt + 1 - off), left);
+            const bool head = off == 0;
+            t0 = max(off - 1, 0);
+            t1 = off + take - 1;
+            left -= take;
+            off = 0;
+            ++m;
+            if (t1 > t0 || (nt == 0 && head))
+                return true;
+        }
+        return false;
+    }
+    __device__ int item() const { return m - 1; }
+};
+
+__device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
+
+__device__ __forceinline__ bool nonfinite_bf16(uint32_t w)
+{
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return f2_to_bf16x2(__half22float2(*reinterpret_cast<const __half2 *>(&h)));
+}
+
+// Unit cut: block c's first unit.
+__device__ __forceinline__ long long cut(long long total, int c, int g) { return total * c / g; }
+
+template <bool BITS8, int NKB>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared s;
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int nk = plan.nk, stages = plan.stages;
+    uint8_t *q_mem = base, *kv_mem = q_mem + nk * kChunkBytes, *p_mem = kv_mem + stages * nk * kChunkBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(smem_addr(&s.kv_full[i]), kLoadWarps);
+            mbar_init(smem_addr(&s.kv_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&s.s_full[0]), 1);
+        mbar_init(smem_addr(&s.s_full[1]), 1);
+        mbar_init(smem_addr(&s.p_full), kSoftWarps);
+        mbar_init(smem_addr(&s.q_full), kLoadWarps);
+        mbar_init(smem_addr(&s.drained), 1);
+        mbar_init_fence();
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (warp == kMmaWarp)
+        tmem_alloc(smem_addr(&s.tmem), plan.tmem_columns);
+
+    // ---- where this block's units begin: prefix sums of items over requests (in the space of the tiles), then of
+    // units over equal stretches of items, a stretch a thread
+    int *items = reinterpret_cast<int *>(base);
+    {
+        int run = 0;
+        int *warp_sum = reinterpret_cast<int *>(s.sums);
+        for (int at = 0; at < p.n_req; at += kThreads) {
+            const int r = at + tid;
+            const int n = r < p.n_req ? request(p, r).items : 0;
+            int a = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(~0u, a, o);
+                if (lane >= o)
+                    a += u;
+            }
+            if (lane == 31)
+                warp_sum[warp] = a;
+            __syncthreads();
+            int before = run;
+            for (int i = 0; i < kThreads / 32; ++i) {
+                before += i < warp ? warp_sum[i] : 0;
+                run += warp_sum[i];
+            }
+            if (r < p.n_req)
+                items[r] = before + a - n;
+            __syncthreads();
+        }
+        if (tid == 0)
+            items[p.n_req] = run;
+        __syncthreads();
+        const int per = (run + kThreads - 1) / kThreads, lo = min(run, tid * per), hi = min(run, lo + per);
+        auto walk = [&](auto &&visit) {
+            if (lo >= hi)
+                return;
+            int r = 0;  // items[r] <= lo < items[r + 1]
+            for (int top = p.n_req; top - r > 1;) {
+                const int mid = (r + top) >> 1;
+                if (items[mid] <= lo)
+                    r = mid;
+                else
+                    top = mid;
+            }
+            Request q = request(p, r);
+            int m = lo - items[r];
+            for (int i = lo; i < hi; ++i, ++m) {
+                while (m >= q.items) {
+                    q = request(p, ++r);
+                    m = 0;
+                }
+                visit(r, m, item_tiles(p, q, m) + 1);
+            }
+        };
+        long long mine = 0;
+        walk([&](int, int, int units) { mine += units; });
+        long long a = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(~0u, a, o);
+            if (lane >= o)
+                a += u;
+        }
+        if (lane == 31)
+            s.sums[warp] = a;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            before += i < warp ? s.sums[i] : 0;
+            total += s.sums[i];
+        }
+        const long long first = before + a - mine;
+        long long g = total / plan.min_units;
+        g = max(1ll, min(g, (long long)plan.blocks));
+        const long long from = cut(total, blockIdx.x, (int)g);
+        if (blockIdx.x < g && from >= first && from < first + mine) {
+            long long at = first;
+            walk([&](int r, int m, int units) {
+                if (from >= at && from < at + units) {
+                    s.r = r;
+                    s.m = m;
+                    s.off = (int)(from - at);
+                }
+                at += units;
+            });
+        }
+        if (tid == 0)
+            s.total = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const long long total = s.total;
+    const int g = (int)max(1ll, min(total / plan.min_units, (long long)plan.blocks));
+    const int c = blockIdx.x;
+    const long long from = cut(total, c, g), units = c < g ? cut(total, c + 1, g) - from : 0;
+    const uint32_t tmem = s.tmem;
+    bool ok = true;
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------ exponentials and output
+        if (tid == 0)
+            plan.joins[c] = make_int4(0, 0, 0, 0);
+        const uint32_t my_lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const int row = warp * 16 + (lane & 15);  // threads 16-31 hold S, threads 0-15 hold O of the same rows
+        const float f = p.scale * kLog2E;
+        int tile = 0;                             // tiles of the block so far
+        long long unit = from;
+        Walk w(p, s, units);
+        while (ok) {
+            const long long left = w.left;
+            if (!w.next())
+                break;
+            unit += left - w.left;  // one past the segment's last unit
+            const int item_rows = min(kTile, w.q.nq * p.n_heads - w.item() * kTile);
+            const int64_t out_row = (int64_t)w.q.first * p.n_heads + (int64_t)w.item() * kTile;
+            const bool live = row < item_rows;
+            const int token = live ? (w.item() * kTile + row) / p.n_heads : 0;
+            const int seen = live ? visible(p, w.q, token) : 0;
+            const int all_see = visible(p, w.q, (int)((int64_t)w.item() * kTile / p.n_heads));
+            const bool whole = item_rows == kTile;
+            float m = -INFINITY, l = 0.0f;
+            for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
+                const int st = tile % stages, b = tile & 1;
+                // (the loaders' own barrier too: their scales and flags are read below)
+                ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status) &&
+                     mbar_wait(smem_addr(&s.s_full[b]), (tile >> 1) & 1, status);
+                ok = __all_sync(~0u, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float x[2][32];
+                tmem_ld_32x32(my_lanes + b * kTile, x[0]);
+                tmem_ld_32x32(my_lanes + b * kTile + 32, x[1]);
+                tmem_wait_ld();
+                const uint64_t valid = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
+                const float4 *rs = reinterpret_cast<const float4 *>(s.scales[st]);
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    float v = x[i / 32][i % 32] * f;
+                    if (BITS8)
+                        v *= reinterpret_cast<const float *>(rs)[i];
+                    x[i / 32][i % 32] = v;
+                }
+                if (!whole || (t + 1) * kTile > all_see || valid != ~0ull) {
+                    const uint64_t poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[st]);
+                    const int lim = seen - t * kTile;
+                    uint64_t see = lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1;
+                    see &= valid;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        float &v = x[i / 32][i % 32];
+                        if (poison >> i & 1)
+                            v = __int_as_float(0x7fffffff);
+                        if (!(see >> i & 1))
+                            v = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    top = fmaxf(top, x[i / 32][i % 32]);
+                const bool raise = lane >= 16 && top > m + kRaise;  // (-inf > -inf is false)
+                if (__any_sync(~0u, raise)) {
+                    const float m2 = raise ? top : m;
+                    const float down = raise ? exp2_fast(m - m2) : 1.0f;
+                    m = m2;
+                    l *= down;
+                    if (t > w.t0) {
+                        const int pt = tile - 1;
+                        ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const float d0 = __shfl_sync(~0u, down, 16 + lane / 4), d1 = __shfl_sync(~0u, down, 24 + lane / 4);
+                        for (int n = 0; n < p.v_dim; n += 32) {
+                            float o[16];
+                            tmem_ld_16x256(my_lanes + n, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] *= (i & 2) ? d1 : d0;
+                            tmem_st_16x256(my_lanes + n, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                uint32_t pk[32];
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float a = exp2_fast(x[i / 16][2 * i % 32] - ref), bb = exp2_fast(x[i / 16][2 * i % 32 + 1] - ref);
+                    sum += a;
+                    sum += bb;
+                    if (BITS8) {
+                        // a hidden row's scale may be anything: its weight stays 0
+                        a = a == 0.0f ? 0.0f : a * reinterpret_cast<const float *>(rs)[2 * i];
+                        bb = bb == 0.0f ? 0.0f : bb * reinterpret_cast<const float *>(rs)[2 * i + 1];
+                    }
+                    pk[i] = f2_to_bf16x2(make_float2(a, bb));
+                }
+                l += sum;
+                if (tile > 0) {
+                    // P's last reader: the product of the tile before
+                    const int pt = tile - 1;
+                    ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok)
+                        break;
+                }
+                if (lane >= 16) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        *reinterpret_cast<uint4 *>(p_mem + row * 128 + ((u ^ (row & 7)) << 4)) =
+                            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&s.p_full));
+            }
+            if (!ok)
+                break;
+            // ---- output: whole items are finished here, parts go to the workspace
+            const bool done = w.t0 == 0 && w.t1 == w.nt;
+            if (w.t1 > w.t0) {
+                const int pt = tile - 1;
+                ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
+                ok = __all_sync(~0u, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+            }
+            m = __shfl_sync(~0u, m, 16 + (lane & 15));
+            l = __shfl_sync(~0u, l, 16 + (lane & 15));
+            const bool write = live && lane < 16;
+            if (done) {
+                const int head = live ? (w.item() * kTile + row) % p.n_heads : 0;
+                const float sink = p.sink ? __ldg(p.sink + head) * kLog2E : -INFINITY;
+                const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
+                const float down = exp2_fast(m - ref), tot = l * down + exp2_fast(sink - ref);
+                const float inv = tot == 0.0f ? 0.0f : down / tot;
+                if (write && p.lse)
+                    p.lse[out_row + row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
+                uint8_t *dst = static_cast<uint8_t *>(p.out) + (out_row + row) * p.v_dim * 2;
+                for (int n = 0; n < p.v_dim; n += 32) {
+                    float o[32];
+                    if (w.t1 > w.t0) {
+                        tmem_ld_32x32(my_lanes + n, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = 0.0f;
+                    }
+                    if (write)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4 *>(dst + (n + i) * 2) = make_uint4(
+                                f2_to_bf16x2(make_float2(o[i] * inv, o[i + 1] * inv)),
+                                f2_to_bf16x2(make_float2(o[i + 2] * inv, o[i + 3] * inv)),
+                                f2_to_bf16x2(make_float2(o[i + 4] * inv, o[i + 5] * inv)),
+                                f2_to_bf16x2(make_float2(o[i + 6] * inv, o[i + 7] * inv)));
+                }
+            } else {
+                const int64_t slot = 2 * (int64_t)c + (w.t0 == 0 ? 1 : 0);
+                if (write)
+                    plan.part_ml[slot * kTile + row] = make_float2(m, l);
+                float *dst = plan.part_o + (slot * kTile + row) * p.v_dim;
+                for (int n = 0; n < p.v_dim; n += 32) {
+                    float o[32];
+                    tmem_ld_32x32(my_lanes + n, o);
+                    tmem_wait_ld();
+                    if (write)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(dst + n + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+                if (w.t0 == 0 && tid == 0) {
+                    // the item's last unit is the block's last so far plus the tiles it has not taken
+                    const long long last = unit - 1 + (w.nt - w.t1);
+                    plan.joins[c] = make_int4((int)out_row, item_rows, (int)(((last + 1) * g - 1) / total), 1);
+                }
+            }
+            tc_fence_before();
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------ matrix products, issued by one thread
+        if (lane == 0) {
+            const uint32_t q_smem = smem_addr(q_mem), kv_smem = smem_addr(kv_mem), p_smem = smem_addr(p_mem);
+            const uint32_t shape_s = mma_shape(kTile, kTile, false);
+            auto product = [&](int tile, bool first) {  // O (+)= P V
+                const int st = tile % stages;
+                ok = mbar_wait(smem_addr(&s.p_full), tile & 1, status);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                const uint32_t v = kv_smem + st * nk * kChunkBytes;
+                for (int n = 0; n < p.v_dim; n += 256) {
+                    const int w = min(256, p.v_dim - n);
+                    const uint32_t shape = mma_shape(kTile, w, true);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + n, mma_operand(p_smem + k * 32, 16, 1024),
+                                 mma_operand(v + (n / 64) * kChunkBytes + k * 2048, kChunkBytes, 1024), shape, !first || k > 0);
+                }
+                mma_commit(smem_addr(&s.kv_empty[st]));
+            };
+            int tile = 0, segment = 0;
+            Walk w(p, s, units);
+            while (ok && w.next()) {
+                if (w.t1 <= w.t0)
+                    continue;
+                ok = mbar_wait(smem_addr(&s.q_full), segment++ & 1, status);
+                for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
+                    const int st = tile % stages, b = tile & 1;
+                    ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t k_smem = kv_smem + st * nk * kChunkBytes;
+                    for (int ch = 0; ch < nk; ++ch)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + (16u << 16) + b * kTile, mma_operand(q_smem + ch * kChunkBytes + k * 32, 16, 1024),
+                                     mma_operand(k_smem + ch * kChunkBytes + k * 32, 16, 1024), shape_s, ch > 0 || k > 0);
+                    mma_commit(smem_addr(&s.s_full[b]));
+                    if (t > w.t0)
+                        product(tile - 1, t - 1 == w.t0);
+                }
+                if (ok)
+                    product(tile - 1, w.t1 - 1 == w.t0);
+            }
+            // nothing may be in flight when the block frees its memory, a wait that gave up included
+            mma_commit(smem_addr(&s.drained));
+            mbar_wait(smem_addr(&s.drained), 0, status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ rows to shared memory
+        const int lw = warp - kMmaWarp - 1;  // rows 8 lw ... 8 lw + 7 of a tile
+        const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
+        int tile = 0;
+        Walk w(p, s, units);
+        while (ok && w.next()) {
+            if (w.t1 <= w.t0)
+                continue;
+            const int item_rows = min(kTile, w.q.nq * p.n_heads - w.item() * kTile);
+            const int end = visible(p, w.q, last_token(p, w.q, w.item()));
+            const int all_see = visible(p, w.q, (int)((int64_t)w.item() * kTile / p.n_heads));
+            const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+            // queries: the products of the segment before have to be done
+            if (tile > 0) {
+                ok = mbar_wait(smem_addr(&s.kv_empty[(tile - 1) % stages]), ((tile - 1) / stages) & 1, status);
+                ok = __all_sync(~0u, ok);
+                if (!ok)
+                    break;
+            }
+            for (int i = 0; i < 2; ++i) {
+                const int row = lw * 8 + (lane >> 3) + 4 * i;
+                const int flat = w.item() * kTile + row;
+                const uint8_t *src = static_cast<const uint8_t *>(p.q);
+                if (row < item_rows)
+                    src += ((int64_t)(w.q.first + flat / p.n_heads) * p.q_token_stride + (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
+                uint8_t *dst = q_mem + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                for (int ch = 0; ch < NKB; ++ch)
+                    if (ch < nk)
+                        *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes) =
+                            row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128 + (lane & 7) * 16)) : zero4();
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&s.q_full));
+            for (int t = w.t0; t < w.t1; ++t, ++tile) {
+                const int st = tile % stages;
+                uint8_t *dst_tile = kv_mem + st * nk * kChunkBytes;
+                // lane's row of the eight for the page look-up
+                const int my = lane & 7, j = t * kTile + lw * 8 + my;
+                int64_t slot = -1;
+                if (j < end) {
+                    const int page = __ldg(table + j / p.page_size);
+                    if (page >= 0 && page < p.n_pages)
+                        slot = (int64_t)page * p.page_size + j % p.page_size;
+                }
+                const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xffu;
+                const bool check = t * kTile + lw * 8 + 8 > all_see;
+                uint32_t poison = 0;
+                if constexpr (BITS8) {
+                    const int row = lane >> 2, quarter = lane & 3;  // 16 of a chunk's 64 columns
+                    const int64_t at = __shfl_sync(~0u, slot, row);
+                    uint4 v[NKB];
+                    const uint8_t *src = cache + at * p.cache_stride + quarter * 16;
+#pragma unroll
+                    for (int ch = 0; ch < NKB; ++ch)
+                        v[ch] = ch < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 64)) : zero4();
+                    const float sc = slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
+                    if (check) {
+                        bool bad = false;
+#pragma unroll
+                        for (int ch = 0; ch < NKB; ++ch)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t word = (&v[ch].x)[i] & 0x7f7f7f7fu;
+                                bad |= __vcmpeq4(word, 0x7f7f7f7fu) != 0;
+                            }
+                        const uint32_t lanes = __ballot_sync(~0u, bad);
+                        if (lanes >> (lane & ~3) & 0xfu)
+#pragma unroll
+                            for (int ch = 0; ch < NKB; ++ch)
+                                v[ch] = zero4();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            poison |= (lanes >> (4 * i) & 0xfu) ? 1u << i : 0u;
+                    }
+                    if (tile >= stages) {
+                        ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok)
+                            break;
+                    }
+                    if (lane < 8)
+                        s.scales[st][lw * 8 + lane] = sc;
+                    const int r = lw * 8 + row;
+#pragma unroll
+                    for (int ch = 0; ch < NKB; ++ch)
+                        if (ch < nk) {
+                            uint8_t *d = dst_tile + ch * kChunkBytes + r * 128;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t a = i ? v[ch].z : v[ch].x, bb = i ? v[ch].w : v[ch].y;
+                                *reinterpret_cast<uint4 *>(d + (((2 * quarter + i) ^ (r & 7)) << 4)) =
+                                    make_uint4(bf16x2_of_e4m3x2(a & 0xffffu), bf16x2_of_e4m3x2(a >> 16),
+                                               bf16x2_of_e4m3x2(bb & 0xffffu), bf16x2_of_e4m3x2(bb >> 16));
+                            }
+                        }
+                } else {
+                    const int64_t at0 = __shfl_sync(~0u, slot, lane >> 3), at1 = __shfl_sync(~0u, slot, (lane >> 3) + 4);
+                    uint4 v[2][NKB];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int64_t at = i ? at1 : at0;
+                        const uint8_t *src = cache + at * p.cache_stride * 2 + (lane & 7) * 16;
+#pragma unroll
+                        for (int ch = 0; ch < NKB; ++ch)
+                            v[i][ch] = ch < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
+                    }
+                    if (check) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            bool bad = false;
+#pragma unroll
+                            for (int ch = 0; ch < NKB; ++ch)
+                                bad |= nonfinite_bf16(v[i][ch].x) || nonfinite_bf16(v[i][ch].y) ||
+                                       nonfinite_bf16(v[i][ch].z) || nonfinite_bf16(v[i][ch].w);
+                            const uint32_t lanes = __ballot_sync(~0u, bad);
+                            if (lanes >> (lane & ~7) & 0xffu)
+#pragma unroll
+                                for (int ch = 0; ch < NKB; ++ch)
+                                    v[i][ch] = zero4();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                poison |= (lanes >> (8 * k) & 0xffu) ? 1u << (4 * i + k) : 0u;
+                        }
+                    }
+                    if (tile >= stages) {
+                        ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok)
+                            break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = lw * 8 + (lane >> 3) + 4 * i;
+                        uint8_t *d = dst_tile + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+                        for (int ch = 0; ch < NKB; ++ch)
+                            if (ch < nk)
+                                *reinterpret_cast<uint4 *>(d + ch * kChunkBytes) = v[i][ch];
+                    }
+                }
+                if (lane == 0) {
+                    s.valid[st][lw] = (uint8_t)valid;
+                    s.poison[st][lw] = (uint8_t)poison;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&s.kv_full[st]));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tmem, plan.tmem_columns);
+    }
+}
+
+// Joins the parts of the items that cross block boundaries: block (c, y) takes four rows of the item whose first part
+// block c of the kernel above wrote (its slot 1), with the slots 0 of the blocks after it up to the item's last.
+__global__ void __launch_bounds__(512) latent_join_kernel(const AttnParams p, const MmaPlan plan)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x;
+    const int4 j = plan.joins[c];
+    const int row = blockIdx.y * 4 + threadIdx.y;
+    if (!j.w || row >= j.y)
+        return;
+    const int64_t out_row = (int64_t)j.x + row;
+    const int head = (int)(out_row % p.n_heads);
+    const float sink = p.sink ? __ldg(p.sink + head) * kLog2E : -INFINITY;
+    auto part = [&](int k) { return (k == c ? 2 * (int64_t)c + 1 : 2 * (int64_t)k) * kTile + row; };
+    float top = sink;
+    for (int k = c; k <= j.z; ++k)
+        top = fmaxf(top, plan.part_ml[part(k)].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float tot = exp2_fast(sink - ref);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int col = threadIdx.x * 4;
+    for (int k = c; k <= j.z; ++k) {
+        const int64_t at = part(k);
+        const float2 ml = plan.part_ml[at];
+        const float w = exp2_fast(ml.x - ref);
+        tot = fmaf(w, ml.y, tot);
+        if (col < p.v_dim) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(plan.part_o + at * p.v_dim + col));
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+    }
+    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+    if (col < p.v_dim)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + out_row * p.v_dim + col) =
+            make_uint2(f2_to_bf16x2(make_float2(o.x * inv, o.y * inv)), f2_to_bf16x2(make_float2(o.z * inv, o.w * inv)));
+    if (p.lse && threadIdx.x == 0)
+        p.lse[out_row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
+}
+
+template <bool BITS8, int NKB>
+cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaStream_t st)
+{
+    auto kern = latent_mma_kernel<BITS8, NKB>;
+    cudaError_t e = allow_max_smem(reinterpret_cast<const void *>(kern));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = dim3(plan.blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = plan.smem;
+    e = cudaLaunchKernelEx(&cfg, kern, p, plan, status);
+    if (e != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(plan.blocks, kTile / 4);
+    cfg.blockDim = dim3((p.v_dim + 3) / 4, 4);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, plan);
+}
+
+MmaPlan make_plan(const AttnParams &p, int num_sms)
+{
+    constexpr size_t kLimit = 227 * 1024 - sizeof(Shared);
+    MmaPlan m{};
+    m.nk = p.head_dim / 64;
+    const size_t fixed = (size_t)(m.nk + 1) * kChunkBytes + 1024;  // queries, P, alignment
+    m.stages = (int)((kLimit - fixed) / ((size_t)m.nk * kChunkBytes));
+    m.stages = m.stages > kMaxStages ? kMaxStages : m.stages;
+    m.smem = fixed + (size_t)m.stages * m.nk * kChunkBytes;
+    // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for the offsets of
+    // kMaxRequests requests
+    m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
+    m.tmem_columns = p.v_dim > 256 ? 512 : p.v_dim > 128 ? 256 : 128;
+    m.blocks = num_sms;
+    m.min_units = 4;
+    return m;
+}
+
+}  // namespace
+
+bool latent_mma_supported(const AttnParams &p)
+{
+    return p.head_dim % 64 == 0 && p.head_dim <= 576 && p.v_dim % 64 == 0 && p.v_dim <= 512;
+}
+
+size_t latent_mma_workspace(const AttnParams &p, int num_sms)
+{
+    const MmaPlan m = make_plan(p, num_sms);
+    return (size_t)m.blocks * (2 * kTile * ((size_t)p.v_dim * sizeof(float) + sizeof(float2)) + sizeof(int4));
+}
+
+cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms, unsigned *status, cudaStream_t st)
+{
+    MmaPlan m = make_plan(p, num_sms);
+    m.part_o = static_cast<float *>(workspace);
+    m.part_ml = reinterpret_cast<float2 *>(m.part_o + (size_t)m.blocks * 2 * kTile * p.v_dim);
+    m.joins = reinterpret_cast<int4 *>(m.part_ml + (size_t)m.blocks * 2 * kTile);
+    const bool bits8 = p.cache_dtype == CSA_DTYPE_E4M3;
+    if (m.nk <= 4)
+        return bits8 ? go<true, 4>(p, m, status, st) : go<false, 4>(p, m, status, st);
+    return bits8 ? go<true, 9>(p, m, status, st) : go<false, 9>(p, m, status, st);
+}
+
+}  // namespace csa

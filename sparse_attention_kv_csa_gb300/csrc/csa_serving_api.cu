@@ -197,9 +197,9 @@ int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
         return fail_status(CSA_ERR_UNSUPPORTED, "cache_dtype must be bf16 or e4m3 (got %d)", cache_dtype);
     if (!(scale > 0.0f) || !(scale < 3.0e38f))
         return fail_status(CSA_ERR_INVALID_VALUE, "scale must be positive and finite (got %g)", (double)scale);
-    if (n_heads > 4096 || n_tokens * (int64_t)n_heads >= (int64_t(1) << 31) || n_req > (1 << 20))
-        return fail_status(CSA_ERR_TOO_LARGE, "n_heads <= 4096, n_tokens * n_heads < 2^31 and n_req <= 2^20 (got %d, %lld, %d)",
-                           n_heads, (long long)n_tokens, n_req);
+    if (n_heads > 4096 || n_tokens * (int64_t)n_heads >= (int64_t(1) << 31) || n_req > csa::kMaxRequests)
+        return fail_status(CSA_ERR_TOO_LARGE, "n_heads <= 4096, n_tokens * n_heads < 2^31 and n_req <= %d (got %d, %lld, %d)",
+                           csa::kMaxRequests, n_heads, (long long)n_tokens, n_req);
     if (n_pages >= (int64_t(1) << 31) || (int64_t)width * page_size >= (int64_t(1) << 31) ||
         n_pages * page_size >= (int64_t(1) << 31))
         return fail_status(CSA_ERR_TOO_LARGE, "n_pages * page_size and width * page_size must be below 2^31");
@@ -227,7 +227,25 @@ int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
                       cache,   cache_stride,   cache_dtype,   cache_dtype == CSA_DTYPE_E4M3 ? row_scales : nullptr,
                       n_pages, page_size,      block_table,   table_stride, width,       seq_lens, ratio,   scale,    sink,
                       out,     lse};
-    cudaError_t e = csa::launch_attention_plain(p, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!csa::latent_mma_supported(p)) {
+        cudaError_t e = csa::launch_attention_plain(p, st);
+        return e == cudaSuccess ? CSA_OK : cuda_status(e, "attention launch");
+    }
+    int sms = 0;
+    cudaMemPool_t pool = nullptr;
+    unsigned *status = nullptr;
+    cudaError_t e = csa::device_facts(&sms, &pool, &status);
+    if (e != cudaSuccess)
+        return cuda_status(e, "device set-up");
+    void *workspace = nullptr;
+    e = cudaMallocFromPoolAsync(&workspace, csa::latent_mma_workspace(p, sms), pool, st);
+    if (e != cudaSuccess)
+        return cuda_status(e, "attention workspace");
+    e = csa::launch_latent_mma(p, workspace, sms, status, st);
+    cudaError_t e2 = cudaFreeAsync(workspace, st);
+    if (e == cudaSuccess)
+        e = e2;
     return e == cudaSuccess ? CSA_OK : cuda_status(e, "attention launch");
 }
 

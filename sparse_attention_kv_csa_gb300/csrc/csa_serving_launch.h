@@ -81,6 +81,11 @@ struct AttnParams {
     void *out;
     float *lse;
 };
+// Tensor-core kernel: widths in multiples of 64 up to 576 and 512; the workspace holds the parts of split items.
+bool latent_mma_supported(const AttnParams &p);
+size_t latent_mma_workspace(const AttnParams &p, int num_sms);
+cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms, unsigned *status, cudaStream_t st);
+// Every other width.
 cudaError_t launch_attention_plain(const AttnParams &p, cudaStream_t st);
 
 // SM count, workspace pool and status word of the current device (set up on first use).
