@@ -15,14 +15,17 @@
 // two S tiles the upper sixteen.  64 query rows, not 128: O of 128 x 512 alone would fill tensor memory, and a K tile
 // of 576 columns and 128 query rows would not fit shared memory twice.
 //
-// Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs, the
-// others fetch rows: global memory to registers (a tile ahead), 8-bit values widened to bf16 (exact), then to shared memory
-// in the swizzled layout.  8-bit rows carry one scale a row: it multiplies S by column and P before its rounding, so
+// Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs.  bf16
+// rows: warp 5 has TMA write whole boxes of rows that lie together in a page, or any four rows at a time where pages
+// are small or rows end inside the tile (rows that no query of the item sees read as zeros); warps 6-9 bring the next
+// item's queries through registers.  8-bit rows: warps 5-12 bring rows to registers (a tile ahead), widen them to bf16
+// (exact) and write the swizzled layout.  Their scale, one a row, multiplies S by column and P before its rounding, so
 // it costs no precision.
 //
 // Work is cut evenly: item i counts one unit for its queries and output and one for each tile; block c takes the units
 // [c T / G, (c+1) T / G) of the T units.  Items that cross a cut leave (O, m, l) of their parts in the workspace and a
 // second kernel joins them in order.  Nothing else depends on the grid, and no order on timing.
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "csa_launch.h"
@@ -36,8 +39,10 @@ constexpr int kTile = 64;                         // query rows of an item, cach
 constexpr int kChunkBytes = kTile * 128;          // 64 rows x 64 bf16 columns
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
-constexpr int kLoadWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kLoadWarps = 8;                     // 8-bit rows
+constexpr int kTmaWarp = 5;                       // bf16 rows
+constexpr int kQueryWarps = 4;                    // bf16 rows: warps that bring queries
+template <bool BITS8> constexpr int kThreadsOf = 32 * (BITS8 ? kSoftWarps + 1 + kLoadWarps : kTmaWarp + 1 + kQueryWarps);
 constexpr int kMaxStages = 4;
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -48,6 +53,8 @@ struct MmaPlan {
     int stages;
     int blocks;       // G
     int min_units;
+    int p_buffers;    // 1 or 2
+    int box_rows;     // rows of a TMA box (a power of two that divides the page), 0: four rows at a time only
     uint32_t tmem_columns;
     size_t smem;
     float *part_o;    // [2 blocks][64][v_dim]
@@ -56,13 +63,14 @@ struct MmaPlan {
 };
 
 struct Shared {
-    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], p_full, q_full, drained;
-    long long sums[kThreads / 32];
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], p_full[2], q_full, q_empty, flags, drained;
+    long long sums[16];
     long long total;
     int r, m, off;               // where the block's units begin
     uint32_t tmem;
     alignas(16) float scales[kMaxStages][kTile];
-    alignas(8) uint8_t valid[kMaxStages][8], poison[kMaxStages][8];
+    alignas(8) uint8_t valid[kMaxStages][8];  // bit i: row i of the tile is some query's to see
+    alignas(8) uint16_t poison[2][kSoftWarps];
 };
 
 // What an item is made of.
@@ -156,9 +164,12 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
 __device__ __forceinline__ long long cut(long long total, int c, int g) { return total * c / g; }
 
 template <bool BITS8, int NKB>
-__global__ void __launch_bounds__(kThreads, 1)
-latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
+__global__ void __launch_bounds__(kThreadsOf<BITS8>, 1)
+latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant__ CUtensorMap boxes,
+                  const __grid_constant__ CUtensorMap single, unsigned *status)
 {
+    constexpr int kThreads = kThreadsOf<BITS8>;
+    constexpr int kQueryArrivals = BITS8 ? kLoadWarps : kQueryWarps;
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -168,13 +179,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
 
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(smem_addr(&s.kv_full[i]), kLoadWarps);
+            mbar_init(smem_addr(&s.kv_full[i]), BITS8 ? kLoadWarps : 1);
             mbar_init(smem_addr(&s.kv_empty[i]), 1);
         }
         mbar_init(smem_addr(&s.s_full[0]), 1);
         mbar_init(smem_addr(&s.s_full[1]), 1);
-        mbar_init(smem_addr(&s.p_full), kSoftWarps);
-        mbar_init(smem_addr(&s.q_full), kLoadWarps);
+        // (two, by the tile's parity: a warp may be a tile ahead of another)
+        mbar_init(smem_addr(&s.p_full[0]), kSoftWarps);
+        mbar_init(smem_addr(&s.p_full[1]), kSoftWarps);
+        mbar_init(smem_addr(&s.q_full), kQueryArrivals);
+        mbar_init(smem_addr(&s.q_empty), 1);
+        mbar_init(smem_addr(&s.flags), kSoftWarps);
         mbar_init(smem_addr(&s.drained), 1);
         mbar_init_fence();
     }
@@ -286,9 +301,11 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
         if (tid == 0)
             plan.joins[c] = make_int4(0, 0, 0, 0);
         const uint32_t my_lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const int row = warp * 16 + (lane & 15);  // threads 16-31 hold S, threads 0-15 hold O of the same rows
+        // S: this thread has columns 8 g + 2 (lane % 4) + {0, 1} of rows r0 (x[4g], x[4g + 1]) and r0 + 8
+        const int r0 = warp * 16 + lane / 4, cq = 2 * (lane & 3);
         const float f = p.scale * kLog2E;
         int tile = 0;                             // tiles of the block so far
+        int flagged = 0;                          // of them, those whose rows were looked through
         long long unit = from;
         Walk w(p, s, units);
         while (ok) {
@@ -298,12 +315,14 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
             unit += left - w.left;  // one past the segment's last unit
             const int item_rows = min(kTile, w.q.nq * p.n_heads - w.item() * kTile);
             const int64_t out_row = (int64_t)w.q.first * p.n_heads + (int64_t)w.item() * kTile;
-            const bool live = row < item_rows;
-            const int token = live ? (w.item() * kTile + row) / p.n_heads : 0;
-            const int seen = live ? visible(p, w.q, token) : 0;
+            auto seen_by = [&](int row) {
+                return row < item_rows ? visible(p, w.q, (w.item() * kTile + row) / p.n_heads) : 0;
+            };
+            const int seen0 = seen_by(r0), seen1 = seen_by(r0 + 8);
             const int all_see = visible(p, w.q, (int)((int64_t)w.item() * kTile / p.n_heads));
+            const int end = visible(p, w.q, last_token(p, w.q, w.item()));
             const bool whole = item_rows == kTile;
-            float m = -INFINITY, l = 0.0f;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // l: this thread's columns only
             for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
                 const int st = tile % stages, b = tile & 1;
                 // (the loaders' own barrier too: their scales and flags are read below)
@@ -313,43 +332,92 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                 if (!ok)
                     break;
                 tc_fence_after();
-                float x[2][32];
-                tmem_ld_32x32(my_lanes + b * kTile, x[0]);
-                tmem_ld_32x32(my_lanes + b * kTile + 32, x[1]);
+                float x[32];
+                tmem_ld_16x256(my_lanes + (16u << 16) + b * kTile, *reinterpret_cast<float(*)[16]>(x));
+                tmem_ld_16x256(my_lanes + (16u << 16) + b * kTile + 32, *reinterpret_cast<float(*)[16]>(x + 16));
                 tmem_wait_ld();
-                const uint64_t valid = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
-                const float4 *rs = reinterpret_cast<const float4 *>(s.scales[st]);
-                float top = -INFINITY;
+                float2 rs[8];
+                if constexpr (BITS8) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    float v = x[i / 32][i % 32] * f;
-                    if (BITS8)
-                        v *= reinterpret_cast<const float *>(rs)[i];
-                    x[i / 32][i % 32] = v;
+                    for (int g8 = 0; g8 < 8; ++g8)
+                        rs[g8] = *reinterpret_cast<const float2 *>(&s.scales[st][8 * g8 + cq]);
                 }
-                if (!whole || (t + 1) * kTile > all_see || valid != ~0ull) {
-                    const uint64_t poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[st]);
-                    const int lim = seen - t * kTile;
-                    uint64_t see = lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1;
-                    see &= valid;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        float &v = x[i / 32][i % 32];
-                        if (poison >> i & 1)
-                            v = __int_as_float(0x7fffffff);
-                        if (!(see >> i & 1))
-                            v = -INFINITY;
+                for (int i = 0; i < 32; ++i) {
+                    x[i] *= f;
+                    if constexpr (BITS8)
+                        x[i] *= (i & 1) ? rs[i / 4].y : rs[i / 4].x;
+                }
+                const uint64_t valid = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
+                if (!whole || (t + 1) * kTile > all_see || valid != ~0ull) {
+                    uint64_t poison = 0;
+                    if (all_see < end && (t + 1) * kTile > all_see) {
+                        // Rows that some queries see and some do not: a weight of zero times an infinity or NaN would
+                        // reach the queries that do not, so such a row is cleared, and the queries that see it get NaN.
+                        const int row = tid >> 1;
+                        uint8_t *mem = kv_mem + st * nk * kChunkBytes + row * 128 + (tid & 1) * 64;
+                        bool bad = false;
+                        if (t * kTile + row >= all_see && t * kTile + row < end)
+                            for (int ch = 0; ch < nk; ++ch)
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kChunkBytes + u * 16);
+                                    bad |= nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w);
+                                }
+                        bad |= __shfl_xor_sync(~0u, (int)bad, 1) != 0;
+                        if (bad)
+                            for (int ch = 0; ch < nk; ++ch)
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    *reinterpret_cast<uint4 *>(mem + ch * kChunkBytes + u * 16) = zero4();
+                        uint32_t two = __ballot_sync(~0u, bad), bits = 0;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            bits |= (two >> (2 * i) & 1u) << i;
+                        // (two sets: a warp writes one again only after every warp has read it)
+                        if (lane == 0) {
+                            s.poison[flagged & 1][warp] = (uint16_t)bits;
+                            mbar_arrive(smem_addr(&s.flags));
+                        }
+                        ok = mbar_wait(smem_addr(&s.flags), flagged & 1, status);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok)
+                            break;
+                        poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[flagged & 1]) >> cq;
+                        ++flagged;
+                    }
+                    auto mask = [&](int seen) {
+                        const int lim = seen - t * kTile;
+                        return (valid & (lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1)) >> cq;
+                    };
+                    const uint64_t see0 = mask(seen0), see1 = mask(seen1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int bit = 8 * (i / 4) + (i & 1);
+                        if (poison >> bit & 1)
+                            x[i] = __int_as_float(0x7fffffff);
+                        if (!(((i & 2) ? see1 : see0) >> bit & 1))
+                            x[i] = -INFINITY;
                     }
                 }
+                float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    top = fmaxf(top, x[i / 32][i % 32]);
-                const bool raise = lane >= 16 && top > m + kRaise;  // (-inf > -inf is false)
-                if (__any_sync(~0u, raise)) {
-                    const float m2 = raise ? top : m;
-                    const float down = raise ? exp2_fast(m - m2) : 1.0f;
-                    m = m2;
-                    l *= down;
+                for (int i = 0; i < 32; i += 4) {
+                    t0 = fmaxf(t0, fmaxf(x[i], x[i + 1]));
+                    t1 = fmaxf(t1, fmaxf(x[i + 2], x[i + 3]));
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, o));
+                    t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, o));
+                }
+                const bool up0 = t0 > m0 + kRaise, up1 = t1 > m1 + kRaise;  // (-inf > -inf is false)
+                if (__any_sync(~0u, up0 || up1)) {
+                    const float d0 = up0 ? exp2_fast(m0 - t0) : 1.0f, d1 = up1 ? exp2_fast(m1 - t1) : 1.0f;
+                    m0 = up0 ? t0 : m0;
+                    m1 = up1 ? t1 : m1;
+                    l0 *= d0;
+                    l1 *= d1;
                     if (t > w.t0) {
                         const int pt = tile - 1;
                         ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
@@ -357,7 +425,6 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                         if (!ok)
                             break;
                         tc_fence_after();
-                        const float d0 = __shfl_sync(~0u, down, 16 + lane / 4), d1 = __shfl_sync(~0u, down, 24 + lane / 4);
                         for (int n = 0; n < p.v_dim; n += 32) {
                             float o[16];
                             tmem_ld_16x256(my_lanes + n, o);
@@ -370,41 +437,43 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                         tmem_wait_st();
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                uint32_t pk[32];
-                float sum = 0.0f;
+                const float ref0 = m0 == -INFINITY ? 0.0f : m0, ref1 = m1 == -INFINITY ? 0.0f : m1;
+                uint32_t pk[16];  // of x[2 i], x[2 i + 1]
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float a = exp2_fast(x[i / 16][2 * i % 32] - ref), bb = exp2_fast(x[i / 16][2 * i % 32 + 1] - ref);
-                    sum += a;
-                    sum += bb;
-                    if (BITS8) {
+                for (int i = 0; i < 16; ++i) {
+                    const float ref = (i & 1) ? ref1 : ref0;
+                    float a = exp2_fast(x[2 * i] - ref), e = exp2_fast(x[2 * i + 1] - ref);
+                    if (i & 1)
+                        l1 += a + e;
+                    else
+                        l0 += a + e;
+                    if constexpr (BITS8) {
                         // a hidden row's scale may be anything: its weight stays 0
-                        a = a == 0.0f ? 0.0f : a * reinterpret_cast<const float *>(rs)[2 * i];
-                        bb = bb == 0.0f ? 0.0f : bb * reinterpret_cast<const float *>(rs)[2 * i + 1];
+                        a = a == 0.0f ? 0.0f : a * rs[i / 2].x;
+                        e = e == 0.0f ? 0.0f : e * rs[i / 2].y;
                     }
-                    pk[i] = f2_to_bf16x2(make_float2(a, bb));
+                    pk[i] = f2_to_bf16x2(make_float2(a, e));
                 }
-                l += sum;
-                if (tile > 0) {
-                    // P's last reader: the product of the tile before
-                    const int pt = tile - 1;
+                if (tile >= plan.p_buffers) {
+                    // the buffer's last reader
+                    const int pt = tile - plan.p_buffers;
                     ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
-                if (lane >= 16) {
+                uint8_t *pw = p_mem + (plan.p_buffers == 2 ? b : 0) * kChunkBytes + r0 * 128 + 2 * cq;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        *reinterpret_cast<uint4 *>(p_mem + row * 128 + ((u ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+                for (int g8 = 0; g8 < 8; ++g8) {
+                    uint8_t *at = pw + ((g8 ^ (r0 & 7)) << 4);
+                    *reinterpret_cast<uint32_t *>(at) = pk[2 * g8];
+                    *reinterpret_cast<uint32_t *>(at + 8 * 128) = pk[2 * g8 + 1];
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&s.p_full));
+                    mbar_arrive(smem_addr(&s.p_full[b]));
             }
             if (!ok)
                 break;
@@ -418,9 +487,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                     break;
                 tc_fence_after();
             }
-            m = __shfl_sync(~0u, m, 16 + (lane & 15));
-            l = __shfl_sync(~0u, l, 16 + (lane & 15));
-            const bool write = live && lane < 16;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                l0 += __shfl_xor_sync(~0u, l0, o);
+                l1 += __shfl_xor_sync(~0u, l1, o);
+            }
+            // O is read a row a thread, by threads 0-15
+            const int row = warp * 16 + (lane & 15), from_lane = 4 * (lane & 7);
+            const float ma = __shfl_sync(~0u, m0, from_lane), mb = __shfl_sync(~0u, m1, from_lane);
+            const float la = __shfl_sync(~0u, l0, from_lane), lb = __shfl_sync(~0u, l1, from_lane);
+            const float m = lane & 8 ? mb : ma, l = lane & 8 ? lb : la;
+            const bool live = row < item_rows, write = live && lane < 16;
             if (done) {
                 const int head = live ? (w.item() * kTile + row) % p.n_heads : 0;
                 const float sink = p.sink ? __ldg(p.sink + head) * kLog2E : -INFINITY;
@@ -478,17 +555,18 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
             const uint32_t shape_s = mma_shape(kTile, kTile, false);
             auto product = [&](int tile, bool first) {  // O (+)= P V
                 const int st = tile % stages;
-                ok = mbar_wait(smem_addr(&s.p_full), tile & 1, status);
+                ok = mbar_wait(smem_addr(&s.p_full[tile & 1]), (tile >> 1) & 1, status);
                 if (!ok)
                     return;
                 tc_fence_after();
                 const uint32_t v = kv_smem + st * nk * kChunkBytes;
+                const uint32_t p_at = p_smem + (plan.p_buffers == 2 ? (tile & 1) * kChunkBytes : 0);
                 for (int n = 0; n < p.v_dim; n += 256) {
                     const int w = min(256, p.v_dim - n);
                     const uint32_t shape = mma_shape(kTile, w, true);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + n, mma_operand(p_smem + k * 32, 16, 1024),
+                        mma_bf16(tmem + n, mma_operand(p_at + k * 32, 16, 1024),
                                  mma_operand(v + (n / 64) * kChunkBytes + k * 2048, kChunkBytes, 1024), shape, !first || k > 0);
                 }
                 mma_commit(smem_addr(&s.kv_empty[st]));
@@ -512,6 +590,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                             mma_bf16(tmem + (16u << 16) + b * kTile, mma_operand(q_smem + ch * kChunkBytes + k * 32, 16, 1024),
                                      mma_operand(k_smem + ch * kChunkBytes + k * 32, 16, 1024), shape_s, ch > 0 || k > 0);
                     mma_commit(smem_addr(&s.s_full[b]));
+                    if (t + 1 == w.t1)
+                        mma_commit(smem_addr(&s.q_empty));
                     if (t > w.t0)
                         product(tile - 1, t - 1 == w.t0);
                 }
@@ -523,58 +603,66 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
             mbar_wait(smem_addr(&s.drained), 0, status);
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------ rows to shared memory
-        const int lw = warp - kMmaWarp - 1;  // rows 8 lw ... 8 lw + 7 of a tile
+    } else if (BITS8 || warp != kTmaWarp) {
+        // ------------------------------------------------ queries, and 8-bit rows, through registers
+        const int lw = warp - (BITS8 ? kMmaWarp : kTmaWarp) - 1;
         const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
-        int tile = 0;
+        int tile = 0, segment = 0;
         Walk w(p, s, units);
         while (ok && w.next()) {
             if (w.t1 <= w.t0)
                 continue;
             const int item_rows = min(kTile, w.q.nq * p.n_heads - w.item() * kTile);
-            const int end = visible(p, w.q, last_token(p, w.q, w.item()));
-            const int all_see = visible(p, w.q, (int)((int64_t)w.item() * kTile / p.n_heads));
-            const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
-            // queries: the products of the segment before have to be done
-            if (tile > 0) {
-                ok = mbar_wait(smem_addr(&s.kv_empty[(tile - 1) % stages]), ((tile - 1) / stages) & 1, status);
-                ok = __all_sync(~0u, ok);
-                if (!ok)
-                    break;
-            }
-            for (int i = 0; i < 2; ++i) {
-                const int row = lw * 8 + (lane >> 3) + 4 * i;
-                const int flat = w.item() * kTile + row;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q);
-                if (row < item_rows)
-                    src += ((int64_t)(w.q.first + flat / p.n_heads) * p.q_token_stride + (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
-                uint8_t *dst = q_mem + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+            {
+                // 64 rows, four a warp at a time; the products S of the segment before have to be done
+                constexpr int kTurns = kTile / (4 * kQueryArrivals);
+                uint4 v[kTurns][NKB];
 #pragma unroll
-                for (int ch = 0; ch < NKB; ++ch)
-                    if (ch < nk)
-                        *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes) =
-                            row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128 + (lane & 7) * 16)) : zero4();
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&s.q_full));
-            for (int t = w.t0; t < w.t1; ++t, ++tile) {
-                const int st = tile % stages;
-                uint8_t *dst_tile = kv_mem + st * nk * kChunkBytes;
-                // lane's row of the eight for the page look-up
-                const int my = lane & 7, j = t * kTile + lw * 8 + my;
-                int64_t slot = -1;
-                if (j < end) {
-                    const int page = __ldg(table + j / p.page_size);
-                    if (page >= 0 && page < p.n_pages)
-                        slot = (int64_t)page * p.page_size + j % p.page_size;
+                for (int i = 0; i < kTurns; ++i) {
+                    const int row = (i * kQueryArrivals + lw) * 4 + (lane >> 3), flat = w.item() * kTile + row;
+                    const uint8_t *src = static_cast<const uint8_t *>(p.q) + (lane & 7) * 16;
+                    if (row < item_rows)
+                        src += ((int64_t)(w.q.first + flat / p.n_heads) * p.q_token_stride +
+                                (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
+#pragma unroll
+                    for (int ch = 0; ch < NKB; ++ch)
+                        v[i][ch] = ch < nk && row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
                 }
-                const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xffu;
-                const bool check = t * kTile + lw * 8 + 8 > all_see;
-                uint32_t poison = 0;
-                if constexpr (BITS8) {
+                if (segment > 0) {
+                    ok = mbar_wait(smem_addr(&s.q_empty), (segment - 1) & 1, status);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok)
+                        break;
+                }
+                ++segment;
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                    const int row = (i * kQueryArrivals + lw) * 4 + (lane >> 3);
+                    uint8_t *dst = q_mem + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+#pragma unroll
+                    for (int ch = 0; ch < NKB; ++ch)
+                        if (ch < nk)
+                            *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes) = v[i][ch];
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&s.q_full));
+            }
+            if constexpr (BITS8) {
+                const int end = visible(p, w.q, last_token(p, w.q, w.item()));
+                const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+                for (int t = w.t0; t < w.t1; ++t, ++tile) {
+                    const int st = tile % stages;
+                    // the warp's rows 8 lw ... 8 lw + 7 of the tile: lane % 8 looks one up
+                    const int j = t * kTile + lw * 8 + (lane & 7);
+                    int64_t slot = -1;
+                    if (j < end) {
+                        const int page = __ldg(table + j / p.page_size);
+                        if (page >= 0 && page < p.n_pages)
+                            slot = (int64_t)page * p.page_size + j % p.page_size;
+                    }
+                    const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xffu;
                     const int row = lane >> 2, quarter = lane & 3;  // 16 of a chunk's 64 columns
                     const int64_t at = __shfl_sync(~0u, slot, row);
                     uint4 v[NKB];
@@ -583,24 +671,6 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                     for (int ch = 0; ch < NKB; ++ch)
                         v[ch] = ch < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 64)) : zero4();
                     const float sc = slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
-                    if (check) {
-                        bool bad = false;
-#pragma unroll
-                        for (int ch = 0; ch < NKB; ++ch)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t word = (&v[ch].x)[i] & 0x7f7f7f7fu;
-                                bad |= __vcmpeq4(word, 0x7f7f7f7fu) != 0;
-                            }
-                        const uint32_t lanes = __ballot_sync(~0u, bad);
-                        if (lanes >> (lane & ~3) & 0xfu)
-#pragma unroll
-                            for (int ch = 0; ch < NKB; ++ch)
-                                v[ch] = zero4();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            poison |= (lanes >> (4 * i) & 0xfu) ? 1u << i : 0u;
-                    }
                     if (tile >= stages) {
                         ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
                         ok = __all_sync(~0u, ok);
@@ -610,73 +680,86 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, unsigned *status)
                     if (lane < 8)
                         s.scales[st][lw * 8 + lane] = sc;
                     const int r = lw * 8 + row;
+                    uint8_t *dst = kv_mem + st * nk * kChunkBytes + r * 128;
 #pragma unroll
                     for (int ch = 0; ch < NKB; ++ch)
-                        if (ch < nk) {
-                            uint8_t *d = dst_tile + ch * kChunkBytes + r * 128;
+                        if (ch < nk)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t a = i ? v[ch].z : v[ch].x, bb = i ? v[ch].w : v[ch].y;
-                                *reinterpret_cast<uint4 *>(d + (((2 * quarter + i) ^ (r & 7)) << 4)) =
+                                const uint32_t a = i ? v[ch].z : v[ch].x, e = i ? v[ch].w : v[ch].y;
+                                *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes + (((2 * quarter + i) ^ (r & 7)) << 4)) =
                                     make_uint4(bf16x2_of_e4m3x2(a & 0xffffu), bf16x2_of_e4m3x2(a >> 16),
-                                               bf16x2_of_e4m3x2(bb & 0xffffu), bf16x2_of_e4m3x2(bb >> 16));
+                                               bf16x2_of_e4m3x2(e & 0xffffu), bf16x2_of_e4m3x2(e >> 16));
                             }
-                        }
-                } else {
-                    const int64_t at0 = __shfl_sync(~0u, slot, lane >> 3), at1 = __shfl_sync(~0u, slot, (lane >> 3) + 4);
-                    uint4 v[2][NKB];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int64_t at = i ? at1 : at0;
-                        const uint8_t *src = cache + at * p.cache_stride * 2 + (lane & 7) * 16;
-#pragma unroll
-                        for (int ch = 0; ch < NKB; ++ch)
-                            v[i][ch] = ch < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
-                    }
-                    if (check) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            bool bad = false;
-#pragma unroll
-                            for (int ch = 0; ch < NKB; ++ch)
-                                bad |= nonfinite_bf16(v[i][ch].x) || nonfinite_bf16(v[i][ch].y) ||
-                                       nonfinite_bf16(v[i][ch].z) || nonfinite_bf16(v[i][ch].w);
-                            const uint32_t lanes = __ballot_sync(~0u, bad);
-                            if (lanes >> (lane & ~7) & 0xffu)
-#pragma unroll
-                                for (int ch = 0; ch < NKB; ++ch)
-                                    v[i][ch] = zero4();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                poison |= (lanes >> (8 * k) & 0xffu) ? 1u << (4 * i + k) : 0u;
-                        }
-                    }
-                    if (tile >= stages) {
-                        ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
-                        ok = __all_sync(~0u, ok);
-                        if (!ok)
-                            break;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = lw * 8 + (lane >> 3) + 4 * i;
-                        uint8_t *d = dst_tile + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-#pragma unroll
-                        for (int ch = 0; ch < NKB; ++ch)
-                            if (ch < nk)
-                                *reinterpret_cast<uint4 *>(d + ch * kChunkBytes) = v[i][ch];
-                    }
+                    if (lane == 0)
+                        s.valid[st][lw] = (uint8_t)valid;
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&s.kv_full[st]));
                 }
-                if (lane == 0) {
-                    s.valid[st][lw] = (uint8_t)valid;
-                    s.poison[st][lw] = (uint8_t)poison;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&s.kv_full[st]));
             }
         }
+    } else if constexpr (!BITS8) {
+        // ------------------------------------------------ bf16 rows by TMA
+        const uint32_t kv_smem = smem_addr(kv_mem);
+        const int none = (int)(p.n_pages * p.page_size);  // a row past the end reads as zeros
+        int tile = 0;
+        Walk w(p, s, units);
+        while (ok && w.next()) {
+            const int end = visible(p, w.q, last_token(p, w.q, w.item()));
+            const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+            for (int t = w.t0; t < w.t1; ++t, ++tile) {
+                const int st = tile % stages;
+                auto look_up = [&](int j) {
+                    if (j < end) {
+                        const int page = __ldg(table + j / p.page_size);
+                        if (page >= 0 && page < p.n_pages)
+                            return page * p.page_size + j % p.page_size;
+                    }
+                    return none;
+                };
+                const int lo = look_up(t * kTile + lane), hi = look_up(t * kTile + 32 + lane);
+                const uint32_t valid_lo = __ballot_sync(~0u, lo != none), valid_hi = __ballot_sync(~0u, hi != none);
+                if (tile >= stages) {
+                    ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok)
+                        break;
+                }
+                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * nk * kChunkBytes;
+                if (lane == 0) {
+                    *reinterpret_cast<uint64_t *>(s.valid[st]) = (uint64_t)valid_hi << 32 | valid_lo;
+                    mbar_arrive_expect_tx(bar, nk * kChunkBytes);
+                }
+                __syncwarp();
+                if (plan.box_rows > 0 && (valid_lo & valid_hi) == ~0u) {
+                    const int runs = kTile / plan.box_rows;
+                    for (int i = lane; i < ((runs * nk + 31) & ~31); i += 32) {
+                        const int ch = i / runs, run = i % runs, row = run * plan.box_rows;
+                        const int a = __shfl_sync(~0u, lo, row & 31), e = __shfl_sync(~0u, hi, row & 31);
+                        if (ch < nk)
+                            tma_load_2d(dst + ch * kChunkBytes + row * 128, &boxes, ch * 64, row < 32 ? a : e, bar);
+                    }
+                } else {
+                    const int four = lane & 15;  // rows 4 four ... 4 four + 3, every second chunk
+                    int r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = four * 4 + k;
+                        const int a = __shfl_sync(~0u, lo, row & 31), e = __shfl_sync(~0u, hi, row & 31);
+                        r[k] = row < 32 ? a : e;
+                    }
+                    for (int ch = lane >> 4; ch < nk; ch += 2)
+                        tma_gather4(dst + ch * kChunkBytes + four * 512, &single, ch * 64, r[0], r[1], r[2], r[3], bar);
+                }
+            }
+        }
+        // no copy outlives the block, after a wait that gave up either
+        if (lane == 0)
+            for (int k = max(0, tile - stages); k < tile; ++k)
+                mbar_wait(smem_addr(&s.kv_full[k % stages]), (k / stages) & 1, status);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -734,6 +817,13 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
 {
     auto kern = latent_mma_kernel<BITS8, NKB>;
     cudaError_t e = allow_max_smem(reinterpret_cast<const void *>(kern));
+    CUtensorMap boxes = {}, single = {};
+    if (!BITS8 && e == cudaSuccess && p.n_pages > 0 && p.width > 0) {
+        const int64_t rows = p.n_pages * p.page_size;
+        e = make_tensor_map_rows(&single, p.cache, rows, p.head_dim, p.cache_stride, 1);
+        if (e == cudaSuccess && plan.box_rows > 0)
+            e = make_tensor_map_rows(&boxes, p.cache, rows, p.head_dim, p.cache_stride, plan.box_rows);
+    }
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -742,9 +832,9 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     cfg.numAttrs = 1;
     cfg.stream = st;
     cfg.gridDim = dim3(plan.blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreadsOf<BITS8>);
     cfg.dynamicSmemBytes = plan.smem;
-    e = cudaLaunchKernelEx(&cfg, kern, p, plan, status);
+    e = cudaLaunchKernelEx(&cfg, kern, p, plan, boxes, single, status);
     if (e != cudaSuccess)
         return e;
     cfg.gridDim = dim3(plan.blocks, kTile / 4);
@@ -762,6 +852,10 @@ MmaPlan make_plan(const AttnParams &p, int num_sms)
     m.stages = (int)((kLimit - fixed) / ((size_t)m.nk * kChunkBytes));
     m.stages = m.stages > kMaxStages ? kMaxStages : m.stages;
     m.smem = fixed + (size_t)m.stages * m.nk * kChunkBytes;
+    m.p_buffers = m.smem + kChunkBytes <= kLimit ? 2 : 1;
+    m.smem += (m.p_buffers - 1) * kChunkBytes;
+    for (m.box_rows = kTile; p.page_size % m.box_rows; m.box_rows /= 2) {}
+    m.box_rows = m.box_rows < 8 ? 0 : m.box_rows;  // eight rows are the swizzle's period
     // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for the offsets of
     // kMaxRequests requests
     m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;

@@ -102,6 +102,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
 // Shared-memory writes of this thread become visible to the tensor cores and bulk copies.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Four rows (any indices; one past the end reads zeros) of a 2-D tensor map whose box is one row of 128 bytes.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int x, int r0, int r1, int r2, int r3, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;

@@ -230,3 +230,20 @@ def test_repeats_side_stream_and_graph(dim):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o3, want[0]) and torch.equal(l3, want[1])
+
+
+def test_cache_without_pages():
+    a = made([40], [1], 8, 512, 1, 16, seed=15)
+    a["cache"] = a["cache"][:0]
+    out, lse = csa.latent_attention(**a)
+    assert (out == 0).all() and torch.isinf(lse).all()
+
+
+def test_items_in_a_row_with_few_live_rows():
+    # one block takes both requests: the warp that writes the first one's output comes a tile later to the second
+    for seed in range(6):
+        a = made([77, 130], [1, 3], 8, 512, 1, 64, seed=seed)
+        out, lse = check(a)
+        for _ in range(5):
+            o2, l2 = csa.latent_attention(**a)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
