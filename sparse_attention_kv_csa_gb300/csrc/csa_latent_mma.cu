@@ -549,59 +549,79 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             tc_fence_before();
         }
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ matrix products, issued by one thread
-        if (lane == 0) {
-            const uint32_t q_smem = smem_addr(q_mem), kv_smem = smem_addr(kv_mem), p_smem = smem_addr(p_mem);
-            const uint32_t shape_s = mma_shape(kTile, kTile, false);
-            auto product = [&](int tile, bool first) {  // O (+)= P V
-                const int st = tile % stages;
-                ok = mbar_wait(smem_addr(&s.p_full[tile & 1]), (tile >> 1) & 1, status);
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint32_t v = kv_smem + st * nk * kChunkBytes;
-                const uint32_t p_at = p_smem + (plan.p_buffers == 2 ? (tile & 1) * kChunkBytes : 0);
+        // ------------------------------------------------ matrix products
+        // The warp stays together and one thread of it issues: the operands of tcgen05.mma are warp-uniform registers,
+        // and a single thread running the loop alone would have each of them moved there, at some 100 cycles an MMA.
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint64_t q_desc = mma_operand(smem_addr(q_mem), 16, 1024), k_desc = mma_operand(smem_addr(kv_mem), 16, 1024);
+        const uint64_t p_desc = mma_operand(smem_addr(p_mem), 16, 1024);
+        const uint64_t v_desc = mma_operand(smem_addr(kv_mem), kChunkBytes, 1024);
+        constexpr uint32_t kStep = kChunkBytes >> 4;  // of a descriptor's address
+        const uint32_t shape_s = mma_shape(kTile, kTile, false);
+        const int stages_u = __shfl_sync(~0u, stages, 0), nk_u = __shfl_sync(~0u, nk, 0);
+        auto product = [&](int tile, int st, bool first) {  // O (+)= P V
+            ok = mbar_wait(smem_addr(&s.p_full[tile & 1]), (tile >> 1) & 1, status);
+            ok = __all_sync(~0u, ok);
+            if (!ok)
+                return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t v = v_desc + (uint32_t)(st * nk_u) * kStep;
+                const uint64_t pa = p_desc + (plan.p_buffers == 2 ? (tile & 1) * kStep : 0);
                 for (int n = 0; n < p.v_dim; n += 256) {
-                    const int w = min(256, p.v_dim - n);
-                    const uint32_t shape = mma_shape(kTile, w, true);
+                    const uint32_t shape = mma_shape(kTile, min(256, p.v_dim - n), true);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + n, mma_operand(p_at + k * 32, 16, 1024),
-                                 mma_operand(v + (n / 64) * kChunkBytes + k * 2048, kChunkBytes, 1024), shape, !first || k > 0);
+                        mma_bf16(tm + n, pa + k * 2, v + (n / 64) * kStep + k * 128, shape, !first || k > 0);
                 }
                 mma_commit(smem_addr(&s.kv_empty[st]));
-            };
-            int tile = 0, segment = 0;
-            Walk w(p, s, units);
-            while (ok && w.next()) {
-                if (w.t1 <= w.t0)
-                    continue;
-                ok = mbar_wait(smem_addr(&s.q_full), segment++ & 1, status);
-                for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
-                    const int st = tile % stages, b = tile & 1;
-                    ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t k_smem = kv_smem + st * nk * kChunkBytes;
-                    for (int ch = 0; ch < nk; ++ch)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + (16u << 16) + b * kTile, mma_operand(q_smem + ch * kChunkBytes + k * 32, 16, 1024),
-                                     mma_operand(k_smem + ch * kChunkBytes + k * 32, 16, 1024), shape_s, ch > 0 || k > 0);
-                    mma_commit(smem_addr(&s.s_full[b]));
-                    if (t + 1 == w.t1)
-                        mma_commit(smem_addr(&s.q_empty));
-                    if (t > w.t0)
-                        product(tile - 1, t - 1 == w.t0);
-                }
-                if (ok)
-                    product(tile - 1, w.t1 - 1 == w.t0);
             }
-            // nothing may be in flight when the block frees its memory, a wait that gave up included
-            mma_commit(smem_addr(&s.drained));
-            mbar_wait(smem_addr(&s.drained), 0, status);
+            __syncwarp();
+        };
+        int tile = 0, segment = 0, st = 0, phase = 0;
+        Walk w(p, s, units);
+        while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
+            const int t0 = __shfl_sync(~0u, w.t0, 0), t1 = __shfl_sync(~0u, w.t1, 0);
+            if (t1 <= t0)
+                continue;
+            ok = mbar_wait(smem_addr(&s.q_full), segment++ & 1, status);
+            ok = __all_sync(~0u, ok);
+            int before = 0;
+            for (int t = t0; t < t1 && ok; ++t, ++tile) {
+                const int b = tile & 1;
+                ok = mbar_wait(smem_addr(&s.kv_full[st]), phase, status);
+                ok = __all_sync(~0u, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t k = k_desc + (uint32_t)(st * nk_u) * kStep;
+                    const uint32_t d = tm + (16u << 16) + b * kTile;
+                    for (int ch = 0; ch < nk_u; ++ch)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16(d, q_desc + ch * kStep + i * 2, k + ch * kStep + i * 2, shape_s, ch > 0 || i > 0);
+                    mma_commit(smem_addr(&s.s_full[b]));
+                    if (t + 1 == t1)
+                        mma_commit(smem_addr(&s.q_empty));
+                }
+                __syncwarp();
+                if (t > t0)
+                    product(tile - 1, before, t - 1 == t0);
+                before = st;
+                if (++st == stages_u) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok)
+                product(tile - 1, before, t1 - 1 == t0);
         }
+        // nothing may be in flight when the block frees its memory, a wait that gave up included
+        if (elect_one())
+            mma_commit(smem_addr(&s.drained));
+        __syncwarp();
+        mbar_wait(smem_addr(&s.drained), 0, status);
         __syncwarp();
     } else if (BITS8 || warp != kTmaWarp) {
         // ------------------------------------------------ queries, and 8-bit rows, through registers
