@@ -1,11 +1,11 @@
 // Attention over a paged cache of shared latent rows on the tensor cores (tcgen05).
 //
 // The query rows of a request are its (token, head) pairs, in order; all of them read the same cache rows.  An item is
-// 64 such rows.  For each tile of 64 cache rows:
+// 64 such rows.  For each tile of 32 cache rows:
 //
-//   S = Q K^T          64 x 64, K = head_dim: both operands K-major in shared memory
+//   S = Q K^T          64 x 32, K = head_dim: both operands K-major in shared memory
 //   P = exp2(S f - m)  f = scale log2 e, m the row's reference; l += sum P; P to bf16 in shared memory
-//   O = O + P V        64 x v_dim, K = 64 cache rows; V is the K tile itself, read with its rows along K
+//   O = O + P V        64 x v_dim, K = 32 cache rows; V is the K tile itself, read with its rows along K
 //
 // so a cache row is fetched once and used for both products.  m is raised (O and l scaled down) only when a logit
 // exceeds it by 2^8: P stays below 2^8, which bf16 and the fp32 sums hold as well as values below one, and O is
@@ -35,15 +35,17 @@
 namespace csa {
 namespace {
 
-constexpr int kTile = 64;                         // query rows of an item, cache rows of a tile
-constexpr int kChunkBytes = kTile * 128;          // 64 rows x 64 bf16 columns
+constexpr int kTile = 64;                         // query rows of an item
+constexpr int kRows = 32;                         // cache rows of a tile
+constexpr int kQueryChunk = kTile * 128;          // bytes of 64 columns of an item's queries
+constexpr int kChunk = kRows * 128;               // bytes of 64 columns of a tile
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
 constexpr int kLoadWarps = 8;                     // 8-bit rows
 constexpr int kTmaWarp = 5;                       // bf16 rows
 constexpr int kQueryWarps = 4;                    // bf16 rows: warps that bring queries
 template <bool BITS8> constexpr int kThreadsOf = 32 * (BITS8 ? kSoftWarps + 1 + kLoadWarps : kTmaWarp + 1 + kQueryWarps);
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 8;
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;                    // log2 of how far a logit may exceed the reference
@@ -53,7 +55,6 @@ struct MmaPlan {
     int stages;
     int blocks;       // G
     int min_units;
-    int p_buffers;    // 1 or 2
     int box_rows;     // rows of a TMA box (a power of two that divides the page), 0: four rows at a time only
     uint32_t tmem_columns;
     size_t smem;
@@ -68,9 +69,10 @@ struct Shared {
     long long total;
     int r, m, off;               // where the block's units begin
     uint32_t tmem;
-    alignas(16) float scales[kMaxStages][kTile];
-    alignas(8) uint8_t valid[kMaxStages][8];  // bit i: row i of the tile is some query's to see
-    alignas(8) uint16_t poison[2][kSoftWarps];
+    alignas(16) float scales[kMaxStages][kRows];
+    // rows of the tile that some query sees: 32 bits (bf16 rows), or four bits a byte
+    alignas(8) uint8_t valid[kMaxStages][8];
+    alignas(4) uint8_t poison[2][kSoftWarps];
 };
 
 // What an item is made of.
@@ -106,7 +108,7 @@ __device__ __forceinline__ int last_token(const AttnParams &p, const Request &q,
 
 __device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
 {
-    return (visible(p, q, last_token(p, q, m)) + kTile - 1) / kTile;
+    return (visible(p, q, last_token(p, q, m)) + kRows - 1) / kRows;
 }
 
 // The block's segments, walked alike by every role.
@@ -174,7 +176,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
     __shared__ Shared s;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int nk = plan.nk, stages = plan.stages;
-    uint8_t *q_mem = base, *kv_mem = q_mem + nk * kChunkBytes, *p_mem = kv_mem + stages * nk * kChunkBytes;
+    // P: rows of 128 bytes, the even tiles' 32 columns in the first half, the odd tiles' in the second
+    uint8_t *q_mem = base, *p_mem = q_mem + nk * kQueryChunk, *kv_mem = p_mem + kQueryChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
@@ -332,67 +335,78 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 if (!ok)
                     break;
                 tc_fence_after();
-                float x[32];
-                tmem_ld_16x256(my_lanes + (16u << 16) + b * kTile, *reinterpret_cast<float(*)[16]>(x));
-                tmem_ld_16x256(my_lanes + (16u << 16) + b * kTile + 32, *reinterpret_cast<float(*)[16]>(x + 16));
+                float x[16];
+                tmem_ld_16x256(my_lanes + (16u << 16) + b * kRows, x);
                 tmem_wait_ld();
-                float2 rs[8];
+                float2 rs[4];
                 if constexpr (BITS8) {
 #pragma unroll
-                    for (int g8 = 0; g8 < 8; ++g8)
+                    for (int g8 = 0; g8 < 4; ++g8)
                         rs[g8] = *reinterpret_cast<const float2 *>(&s.scales[st][8 * g8 + cq]);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     x[i] *= f;
                     if constexpr (BITS8)
                         x[i] *= (i & 1) ? rs[i / 4].y : rs[i / 4].x;
                 }
-                const uint64_t valid = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
-                if (!whole || (t + 1) * kTile > all_see || valid != ~0ull) {
-                    uint64_t poison = 0;
-                    if (all_see < end && (t + 1) * kTile > all_see) {
+                uint32_t valid;
+                if constexpr (BITS8) {
+                    const uint64_t v = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
+                    valid = ~0u;
+                    if (v != 0x0f0f0f0f0f0f0f0full) {
+                        valid = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            valid |= (uint32_t)(v >> (8 * i) & 0xf) << (4 * i);
+                    }
+                } else {
+                    valid = *reinterpret_cast<const volatile uint32_t *>(s.valid[st]);
+                }
+                if (!whole || (t + 1) * kRows > all_see || valid != ~0u) {
+                    uint32_t poison = 0;
+                    if (all_see < end && (t + 1) * kRows > all_see) {
                         // Rows that some queries see and some do not: a weight of zero times an infinity or NaN would
                         // reach the queries that do not, so such a row is cleared, and the queries that see it get NaN.
-                        const int row = tid >> 1;
-                        uint8_t *mem = kv_mem + st * nk * kChunkBytes + row * 128 + (tid & 1) * 64;
+                        const int row = tid >> 2;
+                        uint8_t *mem = kv_mem + st * nk * kChunk + row * 128 + (tid & 3) * 32;
                         bool bad = false;
-                        if (t * kTile + row >= all_see && t * kTile + row < end)
+                        if (t * kRows + row >= all_see && t * kRows + row < end)
                             for (int ch = 0; ch < nk; ++ch)
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kChunkBytes + u * 16);
+                                for (int u = 0; u < 2; ++u) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kChunk + u * 16);
                                     bad |= nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w);
                                 }
-                        bad |= __shfl_xor_sync(~0u, (int)bad, 1) != 0;
-                        if (bad)
+                        const uint32_t lanes = __ballot_sync(~0u, bad);
+                        if (lanes >> (lane & ~3) & 0xfu)
                             for (int ch = 0; ch < nk; ++ch)
 #pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    *reinterpret_cast<uint4 *>(mem + ch * kChunkBytes + u * 16) = zero4();
-                        uint32_t two = __ballot_sync(~0u, bad), bits = 0;
+                                for (int u = 0; u < 2; ++u)
+                                    *reinterpret_cast<uint4 *>(mem + ch * kChunk + u * 16) = zero4();
+                        uint32_t bits = 0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            bits |= (two >> (2 * i) & 1u) << i;
+                        for (int i = 0; i < 8; ++i)
+                            bits |= (lanes >> (4 * i) & 0xfu) ? 1u << i : 0u;
                         // (two sets: a warp writes one again only after every warp has read it)
                         if (lane == 0) {
-                            s.poison[flagged & 1][warp] = (uint16_t)bits;
+                            s.poison[flagged & 1][warp] = (uint8_t)bits;
                             mbar_arrive(smem_addr(&s.flags));
                         }
                         ok = mbar_wait(smem_addr(&s.flags), flagged & 1, status);
                         ok = __all_sync(~0u, ok);
                         if (!ok)
                             break;
-                        poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[flagged & 1]) >> cq;
+                        poison = *reinterpret_cast<const volatile uint32_t *>(s.poison[flagged & 1]) >> cq;
                         ++flagged;
                     }
                     auto mask = [&](int seen) {
-                        const int lim = seen - t * kTile;
-                        return (valid & (lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1)) >> cq;
+                        const int lim = seen - t * kRows;
+                        return (valid & (lim <= 0 ? 0u : lim >= 32 ? ~0u : (1u << lim) - 1)) >> cq;
                     };
-                    const uint64_t see0 = mask(seen0), see1 = mask(seen1);
+                    const uint32_t see0 = mask(seen0), see1 = mask(seen1);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         const int bit = 8 * (i / 4) + (i & 1);
                         if (poison >> bit & 1)
                             x[i] = __int_as_float(0x7fffffff);
@@ -402,7 +416,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 }
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
+                for (int i = 0; i < 16; i += 4) {
                     t0 = fmaxf(t0, fmaxf(x[i], x[i + 1]));
                     t1 = fmaxf(t1, fmaxf(x[i + 2], x[i + 3]));
                 }
@@ -438,9 +452,9 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     }
                 }
                 const float ref0 = m0 == -INFINITY ? 0.0f : m0, ref1 = m1 == -INFINITY ? 0.0f : m1;
-                uint32_t pk[16];  // of x[2 i], x[2 i + 1]
+                uint32_t pk[8];  // of x[2 i], x[2 i + 1]
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float ref = (i & 1) ? ref1 : ref0;
                     float a = exp2_fast(x[2 * i] - ref), e = exp2_fast(x[2 * i + 1] - ref);
                     if (i & 1)
@@ -454,18 +468,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     }
                     pk[i] = f2_to_bf16x2(make_float2(a, e));
                 }
-                if (tile >= plan.p_buffers) {
+                if (tile >= 2) {
                     // the buffer's last reader
-                    const int pt = tile - plan.p_buffers;
+                    const int pt = tile - 2;
                     ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
-                uint8_t *pw = p_mem + (plan.p_buffers == 2 ? b : 0) * kChunkBytes + r0 * 128 + 2 * cq;
 #pragma unroll
-                for (int g8 = 0; g8 < 8; ++g8) {
-                    uint8_t *at = pw + ((g8 ^ (r0 & 7)) << 4);
+                for (int g8 = 0; g8 < 4; ++g8) {
+                    uint8_t *at = p_mem + r0 * 128 + (((4 * b + g8) ^ (r0 & 7)) << 4) + 2 * cq;
                     *reinterpret_cast<uint32_t *>(at) = pk[2 * g8];
                     *reinterpret_cast<uint32_t *>(at + 8 * 128) = pk[2 * g8 + 1];
                 }
@@ -555,9 +568,9 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
         const uint64_t q_desc = mma_operand(smem_addr(q_mem), 16, 1024), k_desc = mma_operand(smem_addr(kv_mem), 16, 1024);
         const uint64_t p_desc = mma_operand(smem_addr(p_mem), 16, 1024);
-        const uint64_t v_desc = mma_operand(smem_addr(kv_mem), kChunkBytes, 1024);
-        constexpr uint32_t kStep = kChunkBytes >> 4;  // of a descriptor's address
-        const uint32_t shape_s = mma_shape(kTile, kTile, false);
+        const uint64_t v_desc = mma_operand(smem_addr(kv_mem), kChunk, 1024);
+        constexpr uint32_t kStep = kChunk >> 4, kQueryStep = kQueryChunk >> 4;  // of a descriptor's address
+        const uint32_t shape_s = mma_shape(kTile, kRows, false);
         const int stages_u = __shfl_sync(~0u, stages, 0), nk_u = __shfl_sync(~0u, nk, 0);
         auto product = [&](int tile, int st, bool first) {  // O (+)= P V
             ok = mbar_wait(smem_addr(&s.p_full[tile & 1]), (tile >> 1) & 1, status);
@@ -567,11 +580,11 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t v = v_desc + (uint32_t)(st * nk_u) * kStep;
-                const uint64_t pa = p_desc + (plan.p_buffers == 2 ? (tile & 1) * kStep : 0);
+                const uint64_t pa = p_desc + (tile & 1) * 4;
                 for (int n = 0; n < p.v_dim; n += 256) {
                     const uint32_t shape = mma_shape(kTile, min(256, p.v_dim - n), true);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < kRows / 16; ++k)
                         mma_bf16(tm + n, pa + k * 2, v + (n / 64) * kStep + k * 128, shape, !first || k > 0);
                 }
                 mma_commit(smem_addr(&s.kv_empty[st]));
@@ -596,11 +609,11 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t k = k_desc + (uint32_t)(st * nk_u) * kStep;
-                    const uint32_t d = tm + (16u << 16) + b * kTile;
+                    const uint32_t d = tm + (16u << 16) + b * kRows;
                     for (int ch = 0; ch < nk_u; ++ch)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16(d, q_desc + ch * kStep + i * 2, k + ch * kStep + i * 2, shape_s, ch > 0 || i > 0);
+                            mma_bf16(d, q_desc + ch * kQueryStep + i * 2, k + ch * kStep + i * 2, shape_s, ch > 0 || i > 0);
                     mma_commit(smem_addr(&s.s_full[b]));
                     if (t + 1 == t1)
                         mma_commit(smem_addr(&s.q_empty));
@@ -662,7 +675,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
 #pragma unroll
                     for (int ch = 0; ch < NKB; ++ch)
                         if (ch < nk)
-                            *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes) = v[i][ch];
+                            *reinterpret_cast<uint4 *>(dst + ch * kQueryChunk) = v[i][ch];
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -674,22 +687,24 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
                 for (int t = w.t0; t < w.t1; ++t, ++tile) {
                     const int st = tile % stages;
-                    // the warp's rows 8 lw ... 8 lw + 7 of the tile: lane % 8 looks one up
-                    const int j = t * kTile + lw * 8 + (lane & 7);
+                    // the warp's rows 4 lw ... 4 lw + 3 of the tile: lane % 4 looks one up
+                    const int j = t * kRows + lw * 4 + (lane & 3);
                     int64_t slot = -1;
                     if (j < end) {
                         const int page = __ldg(table + j / p.page_size);
                         if (page >= 0 && page < p.n_pages)
                             slot = (int64_t)page * p.page_size + j % p.page_size;
                     }
-                    const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xffu;
-                    const int row = lane >> 2, quarter = lane & 3;  // 16 of a chunk's 64 columns
+                    const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xfu;
+                    // a lane brings 16 columns of every second chunk
+                    const int row = lane >> 3, odd = lane >> 2 & 1, quarter = lane & 3;
                     const int64_t at = __shfl_sync(~0u, slot, row);
-                    uint4 v[NKB];
-                    const uint8_t *src = cache + at * p.cache_stride + quarter * 16;
+                    constexpr int kHalf = (NKB + 1) / 2;
+                    uint4 v[kHalf];
+                    const uint8_t *src = cache + at * p.cache_stride + odd * 64 + quarter * 16;
 #pragma unroll
-                    for (int ch = 0; ch < NKB; ++ch)
-                        v[ch] = ch < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 64)) : zero4();
+                    for (int i = 0; i < kHalf; ++i)
+                        v[i] = 2 * i + odd < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128)) : zero4();
                     const float sc = slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
                     if (tile >= stages) {
                         ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
@@ -697,17 +712,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         if (!ok)
                             break;
                     }
-                    if (lane < 8)
-                        s.scales[st][lw * 8 + lane] = sc;
-                    const int r = lw * 8 + row;
-                    uint8_t *dst = kv_mem + st * nk * kChunkBytes + r * 128;
+                    if (lane < 4)
+                        s.scales[st][lw * 4 + lane] = sc;
+                    const int r = lw * 4 + row;
+                    uint8_t *dst = kv_mem + (st * nk + odd) * kChunk + r * 128;
 #pragma unroll
-                    for (int ch = 0; ch < NKB; ++ch)
-                        if (ch < nk)
+                    for (int i = 0; i < kHalf; ++i)
+                        if (2 * i + odd < nk)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t a = i ? v[ch].z : v[ch].x, e = i ? v[ch].w : v[ch].y;
-                                *reinterpret_cast<uint4 *>(dst + ch * kChunkBytes + (((2 * quarter + i) ^ (r & 7)) << 4)) =
+                            for (int u = 0; u < 2; ++u) {
+                                const uint32_t a = u ? v[i].z : v[i].x, e = u ? v[i].w : v[i].y;
+                                *reinterpret_cast<uint4 *>(dst + 2 * i * kChunk + (((2 * quarter + u) ^ (r & 7)) << 4)) =
                                     make_uint4(bf16x2_of_e4m3x2(a & 0xffffu), bf16x2_of_e4m3x2(a >> 16),
                                                bf16x2_of_e4m3x2(e & 0xffffu), bf16x2_of_e4m3x2(e >> 16));
                             }
@@ -739,39 +754,36 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     }
                     return none;
                 };
-                const int lo = look_up(t * kTile + lane), hi = look_up(t * kTile + 32 + lane);
-                const uint32_t valid_lo = __ballot_sync(~0u, lo != none), valid_hi = __ballot_sync(~0u, hi != none);
+                const int slot = look_up(t * kRows + lane);
+                const uint32_t valid = __ballot_sync(~0u, slot != none);
                 if (tile >= stages) {
                     ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
-                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * nk * kChunkBytes;
+                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * nk * kChunk;
                 if (lane == 0) {
-                    *reinterpret_cast<uint64_t *>(s.valid[st]) = (uint64_t)valid_hi << 32 | valid_lo;
-                    mbar_arrive_expect_tx(bar, nk * kChunkBytes);
+                    *reinterpret_cast<uint32_t *>(s.valid[st]) = valid;
+                    mbar_arrive_expect_tx(bar, nk * kChunk);
                 }
                 __syncwarp();
-                if (plan.box_rows > 0 && (valid_lo & valid_hi) == ~0u) {
-                    const int runs = kTile / plan.box_rows;
+                if (plan.box_rows > 0 && valid == ~0u) {
+                    const int runs = kRows / plan.box_rows;
                     for (int i = lane; i < ((runs * nk + 31) & ~31); i += 32) {
-                        const int ch = i / runs, run = i % runs, row = run * plan.box_rows;
-                        const int a = __shfl_sync(~0u, lo, row & 31), e = __shfl_sync(~0u, hi, row & 31);
+                        const int ch = i / runs, row = i % runs * plan.box_rows;
+                        const int r = __shfl_sync(~0u, slot, row);
                         if (ch < nk)
-                            tma_load_2d(dst + ch * kChunkBytes + row * 128, &boxes, ch * 64, row < 32 ? a : e, bar);
+                            tma_load_2d(dst + ch * kChunk + row * 128, &boxes, ch * 64, r, bar);
                     }
                 } else {
-                    const int four = lane & 15;  // rows 4 four ... 4 four + 3, every second chunk
+                    const int four = lane & 7;  // rows 4 four ... 4 four + 3, every fourth chunk
                     int r[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int row = four * 4 + k;
-                        const int a = __shfl_sync(~0u, lo, row & 31), e = __shfl_sync(~0u, hi, row & 31);
-                        r[k] = row < 32 ? a : e;
-                    }
-                    for (int ch = lane >> 4; ch < nk; ch += 2)
-                        tma_gather4(dst + ch * kChunkBytes + four * 512, &single, ch * 64, r[0], r[1], r[2], r[3], bar);
+                    for (int k = 0; k < 4; ++k)
+                        r[k] = __shfl_sync(~0u, slot, four * 4 + k);
+                    for (int ch = lane >> 3; ch < nk; ch += 4)
+                        tma_gather4(dst + ch * kChunk + four * 512, &single, ch * 64, r[0], r[1], r[2], r[3], bar);
                 }
             }
         }
@@ -868,20 +880,18 @@ MmaPlan make_plan(const AttnParams &p, int num_sms)
     constexpr size_t kLimit = 227 * 1024 - sizeof(Shared);
     MmaPlan m{};
     m.nk = p.head_dim / 64;
-    const size_t fixed = (size_t)(m.nk + 1) * kChunkBytes + 1024;  // queries, P, alignment
-    m.stages = (int)((kLimit - fixed) / ((size_t)m.nk * kChunkBytes));
+    const size_t fixed = (size_t)(m.nk + 1) * kQueryChunk + 1024;  // queries, P, alignment
+    m.stages = (int)((kLimit - fixed) / ((size_t)m.nk * kChunk));
     m.stages = m.stages > kMaxStages ? kMaxStages : m.stages;
-    m.smem = fixed + (size_t)m.stages * m.nk * kChunkBytes;
-    m.p_buffers = m.smem + kChunkBytes <= kLimit ? 2 : 1;
-    m.smem += (m.p_buffers - 1) * kChunkBytes;
-    for (m.box_rows = kTile; p.page_size % m.box_rows; m.box_rows /= 2) {}
+    m.smem = fixed + (size_t)m.stages * m.nk * kChunk;
+    for (m.box_rows = kRows; p.page_size % m.box_rows; m.box_rows /= 2) {}
     m.box_rows = m.box_rows < 8 ? 0 : m.box_rows;  // eight rows are the swizzle's period
     // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for the offsets of
     // kMaxRequests requests
     m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
     m.tmem_columns = p.v_dim > 256 ? 512 : p.v_dim > 128 ? 256 : 128;
     m.blocks = num_sms;
-    m.min_units = 4;
+    m.min_units = 8;
     return m;
 }
 
