@@ -368,17 +368,19 @@ cudaError_t make_tensor_map_parts(CUtensorMap *m, const void *ptr, int64_t C, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tensor_map_rows(CUtensorMap *m, const void *ptr, int64_t rows, int cols, int64_t stride, int box_rows)
+cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups)
 {
     cudaError_t e;
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn(&e);
     if (e != cudaSuccess)
         return e;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+    if (rows % 8 != 0)
+        return cudaErrorInvalidValue;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)chunks, (cuuint64_t)rows / 8};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, 128, (cuuint64_t)stride * 16};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)chunks, (cuuint32_t)groups};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;

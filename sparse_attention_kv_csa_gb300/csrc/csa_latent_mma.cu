@@ -1,26 +1,29 @@
 // Attention over a paged cache of shared latent rows on the tensor cores (tcgen05).
 //
 // The query rows of a request are its (token, head) pairs, in order; all of them read the same cache rows.  An item is
-// 64 such rows.  For each tile of 32 cache rows:
+// 64 such rows.  For each tile of R = 32, 48 or 64 cache rows:
 //
-//   S = Q K^T          64 x 32, K = head_dim: both operands K-major in shared memory
+//   S = Q K^T          64 x R, K = head_dim: both operands K-major in shared memory
 //   P = exp2(S f - m)  f = scale log2 e, m the row's reference; l += sum P; P to bf16 in shared memory
-//   O = O + P V        64 x v_dim, K = 32 cache rows; V is the K tile itself, read with its rows along K
+//   O = O + P V        64 x v_dim, K = R cache rows; V is the K tile itself, read with its rows along K
 //
 // so a cache row is fetched once and used for both products.  m is raised (O and l scaled down) only when a logit
 // exceeds it by 2^8: P stays below 2^8, which bf16 and the fp32 sums hold as well as values below one, and O is
 // rarely touched outside the tensor core.
 //
 // Tensor memory: a 64-row accumulator takes 16 of each 32 lanes, so O (up to 512 columns) has the lower sixteen and
-// two S tiles the upper sixteen.  64 query rows, not 128: O of 128 x 512 alone would fill tensor memory, and a K tile
+// four S tiles the upper sixteen.  64 query rows, not 128: O of 128 x 512 alone would fill tensor memory, and K tiles
 // of 576 columns and 128 query rows would not fit shared memory twice.
 //
-// Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs.  bf16
-// rows: warp 5 has TMA write whole boxes of rows that lie together in a page, or any four rows at a time where pages
-// are small or rows end inside the tile (rows that no query of the item sees read as zeros); warps 6-9 bring the next
-// item's queries through registers.  8-bit rows: warps 5-12 bring rows to registers (a tile ahead), widen them to bf16
-// (exact) and write the swizzled layout.  Their scale, one a row, multiplies S by column and P before its rounding, so
-// it costs no precision.
+// Shared memory: a tile lies in groups of eight rows, a group chunk by chunk (64 columns), a chunk as eight swizzled rows
+// of 128 bytes, so that one TMA copy brings any run of whole groups with all their columns: the issue of a copy costs
+// some 80 cycles, and a copy a chunk bounded the kernel.
+//
+// Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs.  Pages of
+// whole groups of bf16 rows: warp 5 issues TMA copies, warps 6-9 bring the next item's queries through registers.
+// Other pages, and 8-bit rows: warps 5-12 take turns at the groups, bring them to registers, widen 8-bit values to
+// bf16 (exact) and write the swizzled layout.  An 8-bit row's scale multiplies S by column and P before its rounding,
+// so it costs no precision.
 //
 // Work is cut evenly: item i counts one unit for its queries and output and one for each tile; block c takes the units
 // [c T / G, (c+1) T / G) of the T units.  Items that cross a cut leave (O, m, l) of their parts in the workspace and a
@@ -35,27 +38,29 @@
 namespace csa {
 namespace {
 
+enum Rows { kTma, kRegisters, kBits8 };           // how rows come: TMA copies, through registers, 8 bits through registers
+
 constexpr int kTile = 64;                         // query rows of an item
-constexpr int kRows = 32;                         // cache rows of a tile
 constexpr int kQueryChunk = kTile * 128;          // bytes of 64 columns of an item's queries
-constexpr int kChunk = kRows * 128;               // bytes of 64 columns of a tile
+constexpr int kGroupChunk = 8 * 128;              // bytes of 64 columns of eight rows
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
-constexpr int kLoadWarps = 8;                     // 8-bit rows
-constexpr int kTmaWarp = 5;                       // bf16 rows
-constexpr int kQueryWarps = 4;                    // bf16 rows: warps that bring queries
-template <bool BITS8> constexpr int kThreadsOf = 32 * (BITS8 ? kSoftWarps + 1 + kLoadWarps : kTmaWarp + 1 + kQueryWarps);
-constexpr int kMaxStages = 8;
+constexpr int kLoadWarps = 8;                     // rows through registers
+constexpr int kTmaWarp = 5;                       // rows by TMA
+constexpr int kQueryWarps = 4;                    // rows by TMA: warps that bring queries
+template <Rows ROWS> constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + kLoadWarps);
+constexpr int kMaxStages = 4;
+constexpr int kScores = 4;                        // S tiles in tensor memory
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;                    // log2 of how far a logit may exceed the reference
 
 struct MmaPlan {
-    int nk;           // 64-column chunks of a row
     int stages;
     int blocks;       // G
     int min_units;
-    int box_rows;     // rows of a TMA box (a power of two that divides the page), 0: four rows at a time only
+    int p_buffers;    // 1 or 2
+    int box_groups;   // groups of eight rows of the larger TMA copy
     uint32_t tmem_columns;
     size_t smem;
     float *part_o;    // [2 blocks][64][v_dim]
@@ -64,15 +69,14 @@ struct MmaPlan {
 };
 
 struct Shared {
-    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], p_full[2], q_full, q_empty, flags, drained;
+    uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[kScores], p_full[2], q_full, q_empty, flags, drained;
     long long sums[16];
     long long total;
     int r, m, off;               // where the block's units begin
     uint32_t tmem;
-    alignas(16) float scales[kMaxStages][kRows];
-    // rows of the tile that some query sees: 32 bits (bf16 rows), or four bits a byte
-    alignas(8) uint8_t valid[kMaxStages][8];
-    alignas(4) uint8_t poison[2][kSoftWarps];
+    alignas(16) float scales[kMaxStages][64];
+    alignas(8) uint8_t missing[kMaxStages][8];  // bit i % 8 of byte i / 8: row i of the tile lies in no page of the cache
+    alignas(8) uint16_t poison[2][kSoftWarps];
 };
 
 // What an item is made of.
@@ -106,13 +110,13 @@ __device__ __forceinline__ int last_token(const AttnParams &p, const Request &q,
     return (int)(row / p.n_heads);
 }
 
-__device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
+template <int R> __device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
 {
-    return (visible(p, q, last_token(p, q, m)) + kRows - 1) / kRows;
+    return (visible(p, q, last_token(p, q, m)) + R - 1) / R;
 }
 
 // The block's segments, walked alike by every role.
-struct Walk {
+template <int R> struct Walk {
     const AttnParams &p;
     Request q;
     int r, m, off;
@@ -133,7 +137,7 @@ struct Walk {
                 m = 0;
                 q = request(p, r);
             }
-            nt = item_tiles(p, q, m);
+            nt = item_tiles<R>(p, q, m);
             const int take = (int)min((long long)(nt + 1 - off), left);
             const bool head = off == 0;
             t0 = max(off - 1, 0);
@@ -165,28 +169,29 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
 // Unit cut: block c's first unit.
 __device__ __forceinline__ long long cut(long long total, int c, int g) { return total * c / g; }
 
-template <bool BITS8, int NKB>
-__global__ void __launch_bounds__(kThreadsOf<BITS8>, 1)
+template <Rows ROWS, int NK, int R>
+__global__ void __launch_bounds__(kThreadsOf<ROWS>, 1)
 latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant__ CUtensorMap boxes,
-                  const __grid_constant__ CUtensorMap single, unsigned *status)
+                  const __grid_constant__ CUtensorMap groups, unsigned *status)
 {
-    constexpr int kThreads = kThreadsOf<BITS8>;
-    constexpr int kQueryArrivals = BITS8 ? kLoadWarps : kQueryWarps;
+    constexpr int kThreads = kThreadsOf<ROWS>;
+    constexpr int kQueryArrivals = ROWS == kTma ? kQueryWarps : kLoadWarps;
+    constexpr int kGroups = R / 8;
+    constexpr int kGroupBytes = NK * kGroupChunk, kTileBytes = kGroups * kGroupBytes;
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const int nk = plan.nk, stages = plan.stages;
-    // P: rows of 128 bytes, the even tiles' 32 columns in the first half, the odd tiles' in the second
-    uint8_t *q_mem = base, *p_mem = q_mem + nk * kQueryChunk, *kv_mem = p_mem + kQueryChunk;
+    const int stages = plan.stages;
+    uint8_t *q_mem = base, *p_mem = q_mem + NK * kQueryChunk, *kv_mem = p_mem + plan.p_buffers * kQueryChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(smem_addr(&s.kv_full[i]), BITS8 ? kLoadWarps : 1);
+            mbar_init(smem_addr(&s.kv_full[i]), ROWS == kTma ? 1 : kGroups);
             mbar_init(smem_addr(&s.kv_empty[i]), 1);
         }
-        mbar_init(smem_addr(&s.s_full[0]), 1);
-        mbar_init(smem_addr(&s.s_full[1]), 1);
+        for (int i = 0; i < kScores; ++i)
+            mbar_init(smem_addr(&s.s_full[i]), 1);
         // (two, by the tile's parity: a warp may be a tile ahead of another)
         mbar_init(smem_addr(&s.p_full[0]), kSoftWarps);
         mbar_init(smem_addr(&s.p_full[1]), kSoftWarps);
@@ -251,7 +256,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     q = request(p, ++r);
                     m = 0;
                 }
-                visit(r, m, item_tiles(p, q, m) + 1);
+                visit(r, m, item_tiles<R>(p, q, m) + 1);
             }
         };
         long long mine = 0;
@@ -310,7 +315,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         int tile = 0;                             // tiles of the block so far
         int flagged = 0;                          // of them, those whose rows were looked through
         long long unit = from;
-        Walk w(p, s, units);
+        Walk<R> w(p, s, units);
         while (ok) {
             const long long left = w.left;
             if (!w.next())
@@ -327,86 +332,87 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             const bool whole = item_rows == kTile;
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // l: this thread's columns only
             for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
-                const int st = tile % stages, b = tile & 1;
+                const int st = tile % stages, b = tile & 1, sb = tile % kScores;
                 // (the loaders' own barrier too: their scales and flags are read below)
                 ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status) &&
-                     mbar_wait(smem_addr(&s.s_full[b]), (tile >> 1) & 1, status);
+                     mbar_wait(smem_addr(&s.s_full[sb]), (tile / kScores) & 1, status);
                 ok = __all_sync(~0u, ok);
                 if (!ok)
                     break;
                 tc_fence_after();
-                float x[16];
-                tmem_ld_16x256(my_lanes + (16u << 16) + b * kRows, x);
-                tmem_wait_ld();
-                float2 rs[4];
-                if constexpr (BITS8) {
+                constexpr int N = R / 2;  // values a thread
+                float x[N];
 #pragma unroll
-                    for (int g8 = 0; g8 < 4; ++g8)
+                for (int i = 0; i < R / 32; ++i)
+                    tmem_ld_16x256(my_lanes + (16u << 16) + sb * 64 + 32 * i, x + 16 * i);
+                if constexpr (R % 32 == 16)
+                    tmem_ld_16x256_half(my_lanes + (16u << 16) + sb * 64 + R - 16, x + N - 8);
+                const uint64_t missing = *reinterpret_cast<const volatile uint64_t *>(s.missing[st]);
+                float2 rs[R / 8];
+                if constexpr (ROWS == kBits8) {
+#pragma unroll
+                    for (int g8 = 0; g8 < R / 8; ++g8)
                         rs[g8] = *reinterpret_cast<const float2 *>(&s.scales[st][8 * g8 + cq]);
                 }
+                tmem_wait_ld();
+                if constexpr (ROWS == kBits8) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[i] *= f;
-                    if constexpr (BITS8)
+                    for (int i = 0; i < N; ++i)
                         x[i] *= (i & 1) ? rs[i / 4].y : rs[i / 4].x;
                 }
-                uint32_t valid;
-                if constexpr (BITS8) {
-                    const uint64_t v = *reinterpret_cast<const volatile uint64_t *>(s.valid[st]);
-                    valid = ~0u;
-                    if (v != 0x0f0f0f0f0f0f0f0full) {
-                        valid = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            valid |= (uint32_t)(v >> (8 * i) & 0xf) << (4 * i);
+                if (!whole || (t + 1) * R > all_see || missing) {
+                    if (ROWS == kTma && (t + 1) * R > end) {
+                        // Whole groups were copied: rows that no query sees may hold anything, and a weight of zero
+                        // does not clear an infinity or NaN of theirs.
+                        for (int i = (end - t * R) * (NK * 8) + tid; i < R * (NK * 8); i += 32 * kSoftWarps) {
+                            const int row = i / (NK * 8), unit16 = i % (NK * 8);
+                            *reinterpret_cast<uint4 *>(kv_mem + st * kTileBytes + (row >> 3) * kGroupBytes + (unit16 >> 3) * kGroupChunk +
+                                                       (row & 7) * 128 + (unit16 & 7) * 16) = zero4();
+                        }
                     }
-                } else {
-                    valid = *reinterpret_cast<const volatile uint32_t *>(s.valid[st]);
-                }
-                if (!whole || (t + 1) * kRows > all_see || valid != ~0u) {
-                    uint32_t poison = 0;
-                    if (all_see < end && (t + 1) * kRows > all_see) {
+                    uint64_t poison = 0;
+                    if (all_see < end && (t + 1) * R > all_see) {
                         // Rows that some queries see and some do not: a weight of zero times an infinity or NaN would
                         // reach the queries that do not, so such a row is cleared, and the queries that see it get NaN.
-                        const int row = tid >> 2;
-                        uint8_t *mem = kv_mem + st * nk * kChunk + row * 128 + (tid & 3) * 32;
+                        const int row = tid >> 1;
+                        uint8_t *mem = kv_mem + st * kTileBytes + (row >> 3) * kGroupBytes + (row & 7) * 128 + (tid & 1) * 64;
                         bool bad = false;
-                        if (t * kRows + row >= all_see && t * kRows + row < end)
-                            for (int ch = 0; ch < nk; ++ch)
+                        if (row < R && t * R + row >= all_see && t * R + row < end)
+                            for (int ch = 0; ch < NK; ++ch)
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kChunk + u * 16);
+                                for (int u = 0; u < 4; ++u) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kGroupChunk + u * 16);
                                     bad |= nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w);
                                 }
                         const uint32_t lanes = __ballot_sync(~0u, bad);
-                        if (lanes >> (lane & ~3) & 0xfu)
-                            for (int ch = 0; ch < nk; ++ch)
+                        if (lanes >> (lane & ~1) & 3u)
+                            for (int ch = 0; ch < NK; ++ch)
 #pragma unroll
-                                for (int u = 0; u < 2; ++u)
-                                    *reinterpret_cast<uint4 *>(mem + ch * kChunk + u * 16) = zero4();
+                                for (int u = 0; u < 4; ++u)
+                                    *reinterpret_cast<uint4 *>(mem + ch * kGroupChunk + u * 16) = zero4();
                         uint32_t bits = 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            bits |= (lanes >> (4 * i) & 0xfu) ? 1u << i : 0u;
+                        for (int i = 0; i < 16; ++i)
+                            bits |= (lanes >> (2 * i) & 3u) ? 1u << i : 0u;
                         // (two sets: a warp writes one again only after every warp has read it)
                         if (lane == 0) {
-                            s.poison[flagged & 1][warp] = (uint8_t)bits;
+                            s.poison[flagged & 1][warp] = (uint16_t)bits;
                             mbar_arrive(smem_addr(&s.flags));
                         }
                         ok = mbar_wait(smem_addr(&s.flags), flagged & 1, status);
                         ok = __all_sync(~0u, ok);
                         if (!ok)
                             break;
-                        poison = *reinterpret_cast<const volatile uint32_t *>(s.poison[flagged & 1]) >> cq;
+                        poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[flagged & 1]) >> cq;
                         ++flagged;
                     }
                     auto mask = [&](int seen) {
-                        const int lim = seen - t * kRows;
-                        return (valid & (lim <= 0 ? 0u : lim >= 32 ? ~0u : (1u << lim) - 1)) >> cq;
+                        const int lim = seen - t * R;
+                        return (~missing & (lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1)) >> cq;
                     };
-                    const uint32_t see0 = mask(seen0), see1 = mask(seen1);
+                    const uint64_t see0 = mask(seen0), see1 = mask(seen1);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < N; ++i) {
                         const int bit = 8 * (i / 4) + (i & 1);
                         if (poison >> bit & 1)
                             x[i] = __int_as_float(0x7fffffff);
@@ -416,7 +422,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 }
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
+                for (int i = 0; i < N; i += 4) {
                     t0 = fmaxf(t0, fmaxf(x[i], x[i + 1]));
                     t1 = fmaxf(t1, fmaxf(x[i + 2], x[i + 3]));
                 }
@@ -425,6 +431,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     t0 = fmaxf(t0, __shfl_xor_sync(~0u, t0, o));
                     t1 = fmaxf(t1, __shfl_xor_sync(~0u, t1, o));
                 }
+                t0 *= f;
+                t1 *= f;
                 const bool up0 = t0 > m0 + kRaise, up1 = t1 > m1 + kRaise;  // (-inf > -inf is false)
                 if (__any_sync(~0u, up0 || up1)) {
                     const float d0 = up0 ? exp2_fast(m0 - t0) : 1.0f, d1 = up1 ? exp2_fast(m1 - t1) : 1.0f;
@@ -451,34 +459,38 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         tmem_wait_st();
                     }
                 }
-                const float ref0 = m0 == -INFINITY ? 0.0f : m0, ref1 = m1 == -INFINITY ? 0.0f : m1;
-                uint32_t pk[8];  // of x[2 i], x[2 i + 1]
+                const float2 ff = splat(f), ref0 = splat(m0 == -INFINITY ? 0.0f : -m0), ref1 = splat(m1 == -INFINITY ? 0.0f : -m1);
+                uint32_t pk[N / 2];  // of x[2 i], x[2 i + 1]
+                float2 sum0 = splat(0.0f), sum1 = splat(0.0f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float ref = (i & 1) ? ref1 : ref0;
-                    float a = exp2_fast(x[2 * i] - ref), e = exp2_fast(x[2 * i + 1] - ref);
+                for (int i = 0; i < N / 2; ++i) {
+                    const float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), ff, (i & 1) ? ref1 : ref0);
+                    float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                     if (i & 1)
-                        l1 += a + e;
+                        sum1 = add2(sum1, e);
                     else
-                        l0 += a + e;
-                    if constexpr (BITS8) {
+                        sum0 = add2(sum0, e);
+                    if constexpr (ROWS == kBits8) {
                         // a hidden row's scale may be anything: its weight stays 0
-                        a = a == 0.0f ? 0.0f : a * rs[i / 2].x;
-                        e = e == 0.0f ? 0.0f : e * rs[i / 2].y;
+                        e.x = e.x == 0.0f ? 0.0f : e.x * rs[i / 2].x;
+                        e.y = e.y == 0.0f ? 0.0f : e.y * rs[i / 2].y;
                     }
-                    pk[i] = f2_to_bf16x2(make_float2(a, e));
+                    pk[i] = f2_to_bf16x2(e);
                 }
-                if (tile >= 2) {
+                l0 += sum0.x + sum0.y;
+                l1 += sum1.x + sum1.y;
+                if (tile >= plan.p_buffers) {
                     // the buffer's last reader
-                    const int pt = tile - 2;
+                    const int pt = tile - plan.p_buffers;
                     ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
+                uint8_t *p_at = p_mem + (plan.p_buffers == 2 ? b : 0) * kQueryChunk + r0 * 128 + 2 * cq;
 #pragma unroll
-                for (int g8 = 0; g8 < 4; ++g8) {
-                    uint8_t *at = p_mem + r0 * 128 + (((4 * b + g8) ^ (r0 & 7)) << 4) + 2 * cq;
+                for (int g8 = 0; g8 < R / 8; ++g8) {
+                    uint8_t *at = p_at + ((g8 ^ (r0 & 7)) << 4);
                     *reinterpret_cast<uint32_t *>(at) = pk[2 * g8];
                     *reinterpret_cast<uint32_t *>(at + 8 * 128) = pk[2 * g8 + 1];
                 }
@@ -505,53 +517,58 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 l0 += __shfl_xor_sync(~0u, l0, o);
                 l1 += __shfl_xor_sync(~0u, l1, o);
             }
-            // O is read a row a thread, by threads 0-15
-            const int row = warp * 16 + (lane & 15), from_lane = 4 * (lane & 7);
-            const float ma = __shfl_sync(~0u, m0, from_lane), mb = __shfl_sync(~0u, m1, from_lane);
-            const float la = __shfl_sync(~0u, l0, from_lane), lb = __shfl_sync(~0u, l1, from_lane);
-            const float m = lane & 8 ? mb : ma, l = lane & 8 ? lb : la;
-            const bool live = row < item_rows, write = live && lane < 16;
+            const bool live0 = r0 < item_rows, live1 = r0 + 8 < item_rows;
             if (done) {
-                const int head = live ? (w.item() * kTile + row) % p.n_heads : 0;
-                const float sink = p.sink ? __ldg(p.sink + head) * kLog2E : -INFINITY;
-                const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
-                const float down = exp2_fast(m - ref), tot = l * down + exp2_fast(sink - ref);
-                const float inv = tot == 0.0f ? 0.0f : down / tot;
-                if (write && p.lse)
-                    p.lse[out_row + row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
-                uint8_t *dst = static_cast<uint8_t *>(p.out) + (out_row + row) * p.v_dim * 2;
-                for (int n = 0; n < p.v_dim; n += 32) {
+                // the factor that turns O into the result
+                auto finish = [&](int row, bool live, float m, float l) {
+                    const float sink = live && p.sink ? __ldg(p.sink + (w.item() * kTile + row) % p.n_heads) * kLog2E : -INFINITY;
+                    const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
+                    const float down = exp2_fast(m - ref), tot = l * down + exp2_fast(sink - ref);
+                    if (live && p.lse && (lane & 3) == 0)
+                        p.lse[out_row + row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
+                    return tot == 0.0f ? 0.0f : down / tot;
+                };
+                const float inv0 = finish(r0, live0, m0, l0), inv1 = finish(r0 + 8, live1, m1, l1);
+                uint16_t *dst = static_cast<uint16_t *>(p.out) + (out_row + r0) * p.v_dim + cq;
+                for (int n = 0; n < p.v_dim; n += 64) {
                     float o[32];
                     if (w.t1 > w.t0) {
-                        tmem_ld_32x32(my_lanes + n, o);
+                        tmem_ld_16x256(my_lanes + n, o);
+                        tmem_ld_16x256(my_lanes + n + 32, o + 16);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] = 0.0f;
                     }
-                    if (write)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4 *>(dst + (n + i) * 2) = make_uint4(
-                                f2_to_bf16x2(make_float2(o[i] * inv, o[i + 1] * inv)),
-                                f2_to_bf16x2(make_float2(o[i + 2] * inv, o[i + 3] * inv)),
-                                f2_to_bf16x2(make_float2(o[i + 4] * inv, o[i + 5] * inv)),
-                                f2_to_bf16x2(make_float2(o[i + 6] * inv, o[i + 7] * inv)));
+                    for (int i = 0; i < 32; i += 4) {
+                        if (live0)
+                            *reinterpret_cast<uint32_t *>(dst + n + 2 * i) = f2_to_bf16x2(make_float2(o[i] * inv0, o[i + 1] * inv0));
+                        if (live1)
+                            *reinterpret_cast<uint32_t *>(dst + 8 * p.v_dim + n + 2 * i) =
+                                f2_to_bf16x2(make_float2(o[i + 2] * inv1, o[i + 3] * inv1));
+                    }
                 }
             } else {
                 const int64_t slot = 2 * (int64_t)c + (w.t0 == 0 ? 1 : 0);
-                if (write)
-                    plan.part_ml[slot * kTile + row] = make_float2(m, l);
-                float *dst = plan.part_o + (slot * kTile + row) * p.v_dim;
-                for (int n = 0; n < p.v_dim; n += 32) {
+                if ((lane & 3) == 0) {
+                    plan.part_ml[slot * kTile + r0] = make_float2(m0, l0);
+                    plan.part_ml[slot * kTile + r0 + 8] = make_float2(m1, l1);
+                }
+                float *dst = plan.part_o + (slot * kTile + r0) * p.v_dim + cq;
+                for (int n = 0; n < p.v_dim; n += 64) {
                     float o[32];
-                    tmem_ld_32x32(my_lanes + n, o);
+                    tmem_ld_16x256(my_lanes + n, o);
+                    tmem_ld_16x256(my_lanes + n + 32, o + 16);
                     tmem_wait_ld();
-                    if (write)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(dst + n + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 32; i += 4) {
+                        if (live0)
+                            *reinterpret_cast<float2 *>(dst + n + 2 * i) = make_float2(o[i], o[i + 1]);
+                        if (live1)
+                            *reinterpret_cast<float2 *>(dst + 8 * p.v_dim + n + 2 * i) = make_float2(o[i + 2], o[i + 3]);
+                    }
                 }
                 if (w.t0 == 0 && tid == 0) {
                     // the item's last unit is the block's last so far plus the tiles it has not taken
@@ -566,69 +583,91 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         // The warp stays together and one thread of it issues: the operands of tcgen05.mma are warp-uniform registers,
         // and a single thread running the loop alone would have each of them moved there, at some 100 cycles an MMA.
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-        const uint64_t q_desc = mma_operand(smem_addr(q_mem), 16, 1024), k_desc = mma_operand(smem_addr(kv_mem), 16, 1024);
-        const uint64_t p_desc = mma_operand(smem_addr(p_mem), 16, 1024);
-        const uint64_t v_desc = mma_operand(smem_addr(kv_mem), kChunk, 1024);
-        constexpr uint32_t kStep = kChunk >> 4, kQueryStep = kQueryChunk >> 4;  // of a descriptor's address
-        const uint32_t shape_s = mma_shape(kTile, kRows, false);
-        const int stages_u = __shfl_sync(~0u, stages, 0), nk_u = __shfl_sync(~0u, nk, 0);
-        auto product = [&](int tile, int st, bool first) {  // O (+)= P V
-            ok = mbar_wait(smem_addr(&s.p_full[tile & 1]), (tile >> 1) & 1, status);
-            ok = __all_sync(~0u, ok);
-            if (!ok)
-                return;
+        const int stages_u = __shfl_sync(~0u, stages, 0);
+        const uint64_t q_desc = mma_operand(smem_addr(q_mem), 16, 1024), p_desc = mma_operand(smem_addr(p_mem), 16, 1024);
+        const uint64_t k_desc = mma_operand(smem_addr(kv_mem), 16, kGroupBytes);
+        const uint64_t v_desc = mma_operand(smem_addr(kv_mem), kGroupChunk, kGroupBytes);
+        constexpr uint32_t kTileStep = kTileBytes >> 4, kQueryStep = kQueryChunk >> 4, kChunkStep = kGroupChunk >> 4;
+        constexpr uint32_t kSixteen = 2 * kGroupBytes >> 4;  // (of a descriptor's address) sixteen rows on
+        constexpr uint32_t shape_s = mma_shape(kTile, R, false);
+        auto scores = [&](int tile, int st, bool last) {  // S = Q K^T
             tc_fence_after();
             if (elect_one()) {
-                const uint64_t v = v_desc + (uint32_t)(st * nk_u) * kStep;
-                const uint64_t pa = p_desc + (tile & 1) * 4;
+                const uint64_t k = k_desc + (uint32_t)st * kTileStep;
+                const uint32_t d = tm + (16u << 16) + (tile % kScores) * 64;
+#pragma unroll
+                for (int ch = 0; ch < NK; ++ch)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_bf16(d, q_desc + ch * kQueryStep + i * 2, k + ch * kChunkStep + i * 2, shape_s, ch > 0 || i > 0);
+                mma_commit(smem_addr(&s.s_full[tile % kScores]));
+                if (last)
+                    mma_commit(smem_addr(&s.q_empty));
+            }
+            __syncwarp();
+        };
+        auto product = [&](int tile, int st, bool first) {  // O (+)= P V
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t v = v_desc + (uint32_t)st * kTileStep;
+                const uint64_t pa = p_desc + (plan.p_buffers == 2 ? (tile & 1) * kQueryStep : 0);
                 for (int n = 0; n < p.v_dim; n += 256) {
                     const uint32_t shape = mma_shape(kTile, min(256, p.v_dim - n), true);
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16(tm + n, pa + k * 2, v + (n / 64) * kStep + k * 128, shape, !first || k > 0);
+                    for (int k = 0; k < R / 16; ++k)
+                        mma_bf16(tm + n, pa + k * 2, v + (n / 64) * kChunkStep + k * kSixteen, shape, !first || k > 0);
                 }
                 mma_commit(smem_addr(&s.kv_empty[st]));
             }
             __syncwarp();
         };
-        int tile = 0, segment = 0, st = 0, phase = 0;
-        Walk w(p, s, units);
+        // i: the next tile to score, j <= i the next to multiply, at most kScores behind.  Whichever is ready goes first:
+        // a tile's rows may wait for the product that frees their space.
+        int segment = 0, i = 0, i_st = 0, i_ph = 0, j = 0, j_st = 0;
+        Walk<R> w(p, s, units);
         while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
-            const int t0 = __shfl_sync(~0u, w.t0, 0), t1 = __shfl_sync(~0u, w.t1, 0);
-            if (t1 <= t0)
+            const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
+            if (n <= 0)
                 continue;
             ok = mbar_wait(smem_addr(&s.q_full), segment++ & 1, status);
             ok = __all_sync(~0u, ok);
-            int before = 0;
-            for (int t = t0; t < t1 && ok; ++t, ++tile) {
-                const int b = tile & 1;
-                ok = mbar_wait(smem_addr(&s.kv_full[st]), phase, status);
-                ok = __all_sync(~0u, ok);
+            const int first = j, end = j + n;
+            while (ok && j < end) {
+                const uint32_t kv_bar = smem_addr(&s.kv_full[i_st]), p_bar = smem_addr(&s.p_full[j & 1]);
+                const uint32_t p_ph = (j >> 1) & 1;
+                const bool may_score = i < end && i - j < kScores, may_multiply = j < i;
+                bool score = false;
+                uint64_t since = 0;
+                for (uint32_t spins = 1;; ++spins) {
+                    score = may_score && __all_sync(~0u, mbar_test(kv_bar, i_ph));
+                    if (score || (may_multiply && __all_sync(~0u, mbar_test(p_bar, p_ph))))
+                        break;
+                    if ((spins & 255u) == 0) {
+                        const uint64_t now = __shfl_sync(~0u, global_ns(), 0);
+                        since = since ? since : now;
+                        if (now - since > kWaitLimitNs) {
+                            if (lane == 0)
+                                atomicCAS(status, 0u, kStatusTimeout);
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
                 if (!ok)
                     break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t k = k_desc + (uint32_t)(st * nk_u) * kStep;
-                    const uint32_t d = tm + (16u << 16) + b * kRows;
-                    for (int ch = 0; ch < nk_u; ++ch)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16(d, q_desc + ch * kQueryStep + i * 2, k + ch * kStep + i * 2, shape_s, ch > 0 || i > 0);
-                    mma_commit(smem_addr(&s.s_full[b]));
-                    if (t + 1 == t1)
-                        mma_commit(smem_addr(&s.q_empty));
-                }
-                __syncwarp();
-                if (t > t0)
-                    product(tile - 1, before, t - 1 == t0);
-                before = st;
-                if (++st == stages_u) {
-                    st = 0;
-                    phase ^= 1;
+                if (score) {
+                    scores(i, i_st, i + 1 == end);
+                    ++i;
+                    if (++i_st == stages_u) {
+                        i_st = 0;
+                        i_ph ^= 1;
+                    }
+                } else {
+                    product(j, j_st, j == first);
+                    ++j;
+                    j_st = j_st + 1 == stages_u ? 0 : j_st + 1;
                 }
             }
-            if (ok)
-                product(tile - 1, before, t1 - 1 == t0);
         }
         // nothing may be in flight when the block frees its memory, a wait that gave up included
         if (elect_one())
@@ -636,12 +675,12 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         __syncwarp();
         mbar_wait(smem_addr(&s.drained), 0, status);
         __syncwarp();
-    } else if (BITS8 || warp != kTmaWarp) {
-        // ------------------------------------------------ queries, and 8-bit rows, through registers
-        const int lw = warp - (BITS8 ? kMmaWarp : kTmaWarp) - 1;
+    } else if (ROWS != kTma || warp != kTmaWarp) {
+        // ------------------------------------------------ queries, and rows, through registers
+        const int lw = warp - (ROWS == kTma ? kTmaWarp : kMmaWarp) - 1;
         const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
         int tile = 0, segment = 0;
-        Walk w(p, s, units);
+        Walk<R> w(p, s, units);
         while (ok && w.next()) {
             if (w.t1 <= w.t0)
                 continue;
@@ -649,7 +688,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             {
                 // 64 rows, four a warp at a time; the products S of the segment before have to be done
                 constexpr int kTurns = kTile / (4 * kQueryArrivals);
-                uint4 v[kTurns][NKB];
+                uint4 v[kTurns][NK];
 #pragma unroll
                 for (int i = 0; i < kTurns; ++i) {
                     const int row = (i * kQueryArrivals + lw) * 4 + (lane >> 3), flat = w.item() * kTile + row;
@@ -658,8 +697,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         src += ((int64_t)(w.q.first + flat / p.n_heads) * p.q_token_stride +
                                 (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
 #pragma unroll
-                    for (int ch = 0; ch < NKB; ++ch)
-                        v[i][ch] = ch < nk && row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
+                    for (int ch = 0; ch < NK; ++ch)
+                        v[i][ch] = row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
                 }
                 if (segment > 0) {
                     ok = mbar_wait(smem_addr(&s.q_empty), (segment - 1) & 1, status);
@@ -673,118 +712,125 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     const int row = (i * kQueryArrivals + lw) * 4 + (lane >> 3);
                     uint8_t *dst = q_mem + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
 #pragma unroll
-                    for (int ch = 0; ch < NKB; ++ch)
-                        if (ch < nk)
-                            *reinterpret_cast<uint4 *>(dst + ch * kQueryChunk) = v[i][ch];
+                    for (int ch = 0; ch < NK; ++ch)
+                        *reinterpret_cast<uint4 *>(dst + ch * kQueryChunk) = v[i][ch];
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&s.q_full));
             }
-            if constexpr (BITS8) {
+            if constexpr (ROWS != kTma) {
+                // Groups of eight rows, counted through the block's tiles; the warp takes every eighth.  A lane finds
+                // the place of one row (lane % 8) a turn ahead.
                 const int end = visible(p, w.q, last_token(p, w.q, w.item()));
                 const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
-                for (int t = w.t0; t < w.t1; ++t, ++tile) {
-                    const int st = tile % stages;
-                    // the warp's rows 4 lw ... 4 lw + 3 of the tile: lane % 4 looks one up
-                    const int j = t * kRows + lw * 4 + (lane & 3);
-                    int64_t slot = -1;
-                    if (j < end) {
-                        const int page = __ldg(table + j / p.page_size);
-                        if (page >= 0 && page < p.n_pages)
-                            slot = (int64_t)page * p.page_size + j % p.page_size;
-                    }
-                    const uint32_t valid = __ballot_sync(~0u, slot >= 0) & 0xfu;
-                    // a lane brings 16 columns of every second chunk
-                    const int row = lane >> 3, odd = lane >> 2 & 1, quarter = lane & 3;
-                    const int64_t at = __shfl_sync(~0u, slot, row);
-                    constexpr int kHalf = (NKB + 1) / 2;
-                    uint4 v[kHalf];
-                    const uint8_t *src = cache + at * p.cache_stride + odd * 64 + quarter * 16;
+                const int n_groups = (w.t1 - w.t0) * kGroups;
+                auto look_up = [&](int i) -> int64_t {
+                    const int j = w.t0 * R + i * 8 + (lane & 7);
+                    if (i >= n_groups || j >= end)
+                        return -1;
+                    const int page = __ldg(table + j / p.page_size);
+                    return page >= 0 && page < p.n_pages ? (int64_t)page * p.page_size + j % p.page_size : -2;
+                };
+                int i = (lw - tile * kGroups) & (kLoadWarps - 1);
+                int64_t slot = look_up(i);
+                for (; i < n_groups; i += kLoadWarps) {
+                    const int mine = tile + i / kGroups, gr = i % kGroups, st = mine % stages;
+                    const uint32_t missing = __ballot_sync(~0u, slot == -2) & 0xffu;
+                    constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
+                    uint4 v[kParts][NK];
 #pragma unroll
-                    for (int i = 0; i < kHalf; ++i)
-                        v[i] = 2 * i + odd < nk && at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + i * 128)) : zero4();
-                    const float sc = slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
-                    if (tile >= stages) {
-                        ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
+                    for (int h = 0; h < kParts; ++h) {
+                        const int64_t at = __shfl_sync(~0u, slot, ROWS == kBits8 ? lane >> 2 : (lane >> 3) + 4 * h);
+                        const uint8_t *src = ROWS == kBits8 ? cache + at * p.cache_stride + (lane & 3) * 16
+                                                            : cache + at * p.cache_stride * 2 + (lane & 7) * 16;
+#pragma unroll
+                        for (int ch = 0; ch < NK; ++ch)
+                            v[h][ch] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * (ROWS == kBits8 ? 64 : 128))) : zero4();
+                    }
+                    const float sc = ROWS == kBits8 && slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
+                    slot = look_up(i + kLoadWarps);
+                    if (mine >= stages) {
+                        ok = mbar_wait(smem_addr(&s.kv_empty[st]), (mine / stages - 1) & 1, status);
                         ok = __all_sync(~0u, ok);
                         if (!ok)
                             break;
                     }
-                    if (lane < 4)
-                        s.scales[st][lw * 4 + lane] = sc;
-                    const int r = lw * 4 + row;
-                    uint8_t *dst = kv_mem + (st * nk + odd) * kChunk + r * 128;
+                    uint8_t *dst = kv_mem + st * kTileBytes + gr * kGroupBytes;
+                    if constexpr (ROWS == kBits8) {
+                        if (lane < 8)
+                            s.scales[st][gr * 8 + lane] = sc;
+                        const int r = lane >> 2, quarter = lane & 3;  // 16 of a chunk's 64 columns
 #pragma unroll
-                    for (int i = 0; i < kHalf; ++i)
-                        if (2 * i + odd < nk)
+                        for (int ch = 0; ch < NK; ++ch)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
-                                const uint32_t a = u ? v[i].z : v[i].x, e = u ? v[i].w : v[i].y;
-                                *reinterpret_cast<uint4 *>(dst + 2 * i * kChunk + (((2 * quarter + u) ^ (r & 7)) << 4)) =
+                                const uint32_t a = u ? v[0][ch].z : v[0][ch].x, e = u ? v[0][ch].w : v[0][ch].y;
+                                *reinterpret_cast<uint4 *>(dst + ch * kGroupChunk + r * 128 + (((2 * quarter + u) ^ r) << 4)) =
                                     make_uint4(bf16x2_of_e4m3x2(a & 0xffffu), bf16x2_of_e4m3x2(a >> 16),
                                                bf16x2_of_e4m3x2(e & 0xffffu), bf16x2_of_e4m3x2(e >> 16));
                             }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < kParts; ++h) {
+                            const int r = (lane >> 3) + 4 * h;
+#pragma unroll
+                            for (int ch = 0; ch < NK; ++ch)
+                                *reinterpret_cast<uint4 *>(dst + ch * kGroupChunk + r * 128 + (((lane & 7) ^ r) << 4)) = v[h][ch];
+                        }
+                    }
                     if (lane == 0)
-                        s.valid[st][lw] = (uint8_t)valid;
+                        s.missing[st][gr] = (uint8_t)missing;
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&s.kv_full[st]));
                 }
+                tile += w.t1 - w.t0;
             }
         }
-    } else if constexpr (!BITS8) {
-        // ------------------------------------------------ bf16 rows by TMA
+    } else if constexpr (ROWS == kTma) {
+        // ------------------------------------------------ rows by TMA, in groups of eight
         const uint32_t kv_smem = smem_addr(kv_mem);
-        const int none = (int)(p.n_pages * p.page_size);  // a row past the end reads as zeros
+        const int none = (int)(p.n_pages * p.page_size / 8);  // a group past the end reads as zeros
+        const int copies = kGroups / plan.box_groups;
         int tile = 0;
-        Walk w(p, s, units);
+        Walk<R> w(p, s, units);
         while (ok && w.next()) {
             const int end = visible(p, w.q, last_token(p, w.q, w.item()));
             const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+            // lane % 8 finds the place of one of a tile's groups, a tile ahead
+            auto look_up = [&](int t) {
+                const int j = t * R + (lane & 7) * 8;
+                if (t >= w.t1 || (lane & 7) >= kGroups || j >= end)
+                    return none;
+                const int page = __ldg(table + j / p.page_size);
+                return page >= 0 && page < p.n_pages ? (page * p.page_size + j % p.page_size) >> 3 : -1;
+            };
+            int next = look_up(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
                 const int st = tile % stages;
-                auto look_up = [&](int j) {
-                    if (j < end) {
-                        const int page = __ldg(table + j / p.page_size);
-                        if (page >= 0 && page < p.n_pages)
-                            return page * p.page_size + j % p.page_size;
-                    }
-                    return none;
-                };
-                const int slot = look_up(t * kRows + lane);
-                const uint32_t valid = __ballot_sync(~0u, slot != none);
+                const uint32_t missing = __ballot_sync(~0u, next < 0) & 0xffu;
+                const int at = next < 0 ? none : next;
+                next = look_up(t + 1);
                 if (tile >= stages) {
                     ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
-                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * nk * kChunk;
-                if (lane == 0) {
-                    *reinterpret_cast<uint32_t *>(s.valid[st]) = valid;
-                    mbar_arrive_expect_tx(bar, nk * kChunk);
-                }
+                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * kTileBytes;
+                if (lane < 8)
+                    s.missing[st][lane] = missing >> lane & 1 ? 0xff : 0;
                 __syncwarp();
-                if (plan.box_rows > 0 && valid == ~0u) {
-                    const int runs = kRows / plan.box_rows;
-                    for (int i = lane; i < ((runs * nk + 31) & ~31); i += 32) {
-                        const int ch = i / runs, row = i % runs * plan.box_rows;
-                        const int r = __shfl_sync(~0u, slot, row);
-                        if (ch < nk)
-                            tma_load_2d(dst + ch * kChunk + row * 128, &boxes, ch * 64, r, bar);
-                    }
-                } else {
-                    const int four = lane & 7;  // rows 4 four ... 4 four + 3, every fourth chunk
-                    int r[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        r[k] = __shfl_sync(~0u, slot, four * 4 + k);
-                    for (int ch = lane >> 3; ch < nk; ch += 4)
-                        tma_gather4(dst + ch * kChunk + four * 512, &single, ch * 64, r[0], r[1], r[2], r[3], bar);
-                }
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, kTileBytes);
+                __syncwarp();
+                const bool plain = !missing && (t + 1) * R <= end;  // runs of groups that lie together
+                const int first = __shfl_sync(~0u, at, plain ? (lane & 7) * plan.box_groups & 7 : lane & 7);
+                if (plain ? lane < copies : lane < kGroups)
+                    tma_load_4d(dst + lane * (plain ? plan.box_groups : 1) * kGroupBytes, plain ? &boxes : &groups, 0, 0, 0, first, bar);
             }
         }
         // no copy outlives the block, after a wait that gave up either
@@ -844,17 +890,17 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const AttnParams p, co
         p.lse[out_row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
 }
 
-template <bool BITS8, int NKB>
+template <Rows ROWS, int NK, int R>
 cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaStream_t st)
 {
-    auto kern = latent_mma_kernel<BITS8, NKB>;
+    auto kern = latent_mma_kernel<ROWS, NK, R>;
     cudaError_t e = allow_max_smem(reinterpret_cast<const void *>(kern));
-    CUtensorMap boxes = {}, single = {};
-    if (!BITS8 && e == cudaSuccess && p.n_pages > 0 && p.width > 0) {
+    CUtensorMap boxes = {}, groups = {};
+    if (ROWS == kTma && e == cudaSuccess && p.width > 0) {
         const int64_t rows = p.n_pages * p.page_size;
-        e = make_tensor_map_rows(&single, p.cache, rows, p.head_dim, p.cache_stride, 1);
-        if (e == cudaSuccess && plan.box_rows > 0)
-            e = make_tensor_map_rows(&boxes, p.cache, rows, p.head_dim, p.cache_stride, plan.box_rows);
+        e = make_tensor_map_groups(&groups, p.cache, rows, NK, p.cache_stride, 1);
+        if (e == cudaSuccess)
+            e = make_tensor_map_groups(&boxes, p.cache, rows, NK, p.cache_stride, plan.box_groups);
     }
     if (e != cudaSuccess)
         return e;
@@ -864,9 +910,9 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     cfg.numAttrs = 1;
     cfg.stream = st;
     cfg.gridDim = dim3(plan.blocks);
-    cfg.blockDim = dim3(kThreadsOf<BITS8>);
+    cfg.blockDim = dim3(kThreadsOf<ROWS>);
     cfg.dynamicSmemBytes = plan.smem;
-    e = cudaLaunchKernelEx(&cfg, kern, p, plan, boxes, single, status);
+    e = cudaLaunchKernelEx(&cfg, kern, p, plan, boxes, groups, status);
     if (e != cudaSuccess)
         return e;
     cfg.gridDim = dim3(plan.blocks, kTile / 4);
@@ -875,24 +921,41 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, plan);
 }
 
+constexpr size_t kSmemLimit = 227 * 1024 - sizeof(Shared);
+
+constexpr size_t fixed_of(int nk) { return (size_t)(nk + 1) * kQueryChunk + 1024; }  // queries, P, alignment
+
+constexpr int stages_of(int nk, int rows) { return (int)((kSmemLimit - fixed_of(nk)) / ((size_t)nk * rows * 128)); }
+
+// Rows of a tile: the tensor core wants wide tiles, the loads want three tiles in flight; so 64 where three fit beside
+// the queries, else 48, else (576 columns) 32 in four.
+constexpr int rows_of(int nk) { return stages_of(nk, 64) >= 3 ? 64 : stages_of(nk, 48) >= 3 ? 48 : 32; }
+
 MmaPlan make_plan(const AttnParams &p, int num_sms)
 {
-    constexpr size_t kLimit = 227 * 1024 - sizeof(Shared);
     MmaPlan m{};
-    m.nk = p.head_dim / 64;
-    const size_t fixed = (size_t)(m.nk + 1) * kQueryChunk + 1024;  // queries, P, alignment
-    m.stages = (int)((kLimit - fixed) / ((size_t)m.nk * kChunk));
-    m.stages = m.stages > kMaxStages ? kMaxStages : m.stages;
-    m.smem = fixed + (size_t)m.stages * m.nk * kChunk;
-    for (m.box_rows = kRows; p.page_size % m.box_rows; m.box_rows /= 2) {}
-    m.box_rows = m.box_rows < 8 ? 0 : m.box_rows;  // eight rows are the swizzle's period
+    const int nk = p.head_dim / 64, rows = rows_of(nk);
+    m.stages = stages_of(nk, rows) > kMaxStages ? kMaxStages : stages_of(nk, rows);
+    m.smem = fixed_of(nk) + (size_t)m.stages * nk * rows * 128;
+    m.p_buffers = m.smem + kQueryChunk <= kSmemLimit ? 2 : 1;
+    m.smem += (m.p_buffers - 1) * kQueryChunk;
+    // the larger copy: the most groups that divide both the tile and the page
+    for (m.box_groups = rows / 8; m.box_groups > 1 && (p.page_size % (8 * m.box_groups) || (rows / 8) % m.box_groups); --m.box_groups) {}
     // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for the offsets of
     // kMaxRequests requests
     m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
-    m.tmem_columns = p.v_dim > 256 ? 512 : p.v_dim > 128 ? 256 : 128;
+    m.tmem_columns = p.v_dim > 256 ? 512 : 256;  // O below, the S tiles above
     m.blocks = num_sms;
-    m.min_units = 8;
+    m.min_units = 4;
     return m;
+}
+
+template <int NK> cudaError_t go_rows(const AttnParams &p, const MmaPlan &m, unsigned *status, cudaStream_t st)
+{
+    constexpr int R = rows_of(NK);
+    if (p.cache_dtype == CSA_DTYPE_E4M3)
+        return go<kBits8, NK, R>(p, m, status, st);
+    return p.page_size % 8 == 0 ? go<kTma, NK, R>(p, m, status, st) : go<kRegisters, NK, R>(p, m, status, st);
 }
 
 }  // namespace
@@ -914,10 +977,18 @@ cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms,
     m.part_o = static_cast<float *>(workspace);
     m.part_ml = reinterpret_cast<float2 *>(m.part_o + (size_t)m.blocks * 2 * kTile * p.v_dim);
     m.joins = reinterpret_cast<int4 *>(m.part_ml + (size_t)m.blocks * 2 * kTile);
-    const bool bits8 = p.cache_dtype == CSA_DTYPE_E4M3;
-    if (m.nk <= 4)
-        return bits8 ? go<true, 4>(p, m, status, st) : go<false, 4>(p, m, status, st);
-    return bits8 ? go<true, 9>(p, m, status, st) : go<false, 9>(p, m, status, st);
+    switch (p.head_dim / 64) {
+    case 1: return go_rows<1>(p, m, status, st);
+    case 2: return go_rows<2>(p, m, status, st);
+    case 3: return go_rows<3>(p, m, status, st);
+    case 4: return go_rows<4>(p, m, status, st);
+    case 5: return go_rows<5>(p, m, status, st);
+    case 6: return go_rows<6>(p, m, status, st);
+    case 7: return go_rows<7>(p, m, status, st);
+    case 8: return go_rows<8>(p, m, status, st);
+    case 9: return go_rows<9>(p, m, status, st);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace csa

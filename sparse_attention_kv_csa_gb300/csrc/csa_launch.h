@@ -138,9 +138,10 @@ cudaError_t resident_blocks(const void *fn, int threads, size_t smem, int cluste
 // box_cols] boxes (no swizzle, 256-byte L2 promotion).
 cudaError_t make_tensor_map_2d(CUtensorMap *m, const void *ptr, int64_t C, int box_cols, int box_rows);
 cudaError_t make_tensor_map_3d(CUtensorMap *m, const void *ptr, int64_t C, int chunk_cols, int chunks, int box_rows);
-// Boxes of 64 bf16 columns x box_rows of a [rows, cols] bf16 matrix with the given row stride (elements), 128-byte
-// swizzle; rows past the end read as zeros.
-cudaError_t make_tensor_map_rows(CUtensorMap *m, const void *ptr, int64_t rows, int cols, int64_t stride, int box_rows);
+// A [rows, 64 chunks] bf16 matrix with the given row stride (elements, rows a multiple of 8) seen as [rows / 8]
+// [chunks][8][64]: a box of `groups` groups of eight rows at (0, 0, 0, row / 8) lands, 128-byte swizzled, group by
+// group, in a group chunk by chunk.  Groups past the end read as zeros.
+cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups);
 cudaError_t make_tensor_map_parts(CUtensorMap *m, const void *ptr, int64_t C, int box_cols, int ratio, int head_dim);
 
 // The backward's kernel family and plan for one shape on the current device: one
