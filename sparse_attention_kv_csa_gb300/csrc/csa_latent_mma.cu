@@ -1,7 +1,7 @@
 // Attention over a paged cache of shared latent rows on the tensor cores (tcgen05).
 //
 // The query rows of a request are its (token, head) pairs, in order; all of them read the same cache rows.  An item is
-// 64 such rows.  For each tile of R = 32, 48 or 64 cache rows:
+// 64 such rows.  For each tile of R = 48 or 64 cache rows:
 //
 //   S = Q K^T          64 x R, K = head_dim: both operands K-major in shared memory
 //   P = exp2(S f - m)  f = scale log2 e, m the row's reference; l += sum P; P to bf16 in shared memory
@@ -50,6 +50,8 @@ constexpr int kTmaWarp = 5;                       // rows by TMA
 constexpr int kQueryWarps = 4;                    // rows by TMA: warps that bring queries
 template <Rows ROWS> constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + kLoadWarps);
 constexpr int kMaxStages = 4;
+constexpr int kMinUnits = 4;                      // of a block's share: fewer, larger parts to join
+constexpr int kKept = 4096;                       // requests whose facts are kept in shared memory while work is cut
 constexpr int kScores = 4;                        // S tiles in tensor memory
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -58,7 +60,6 @@ constexpr float kRaise = 8.0f;                    // log2 of how far a logit may
 struct MmaPlan {
     int stages;
     int blocks;       // G
-    int min_units;
     int p_buffers;    // 1 or 2
     int box_groups;   // groups of eight rows of the larger TMA copy
     uint32_t tmem_columns;
@@ -73,6 +74,7 @@ struct Shared {
     long long sums[16];
     long long total;
     int r, m, off;               // where the block's units begin
+    int first[4];                // and the facts of request r
     uint32_t tmem;
     alignas(16) float scales[kMaxStages][64];
     alignas(8) uint8_t missing[kMaxStages][8];  // bit i % 8 of byte i / 8: row i of the tile lies in no page of the cache
@@ -122,10 +124,9 @@ template <int R> struct Walk {
     int r, m, off;
     long long left;
     int nt, t0, t1;
-    __device__ Walk(const AttnParams &p_, const Shared &s, long long units) : p(p_), r(s.r), m(s.m), off(s.off), left(units)
+    __device__ Walk(const AttnParams &p_, const Shared &s, long long units)
+        : p(p_), q{s.first[0], s.first[1], s.first[2], s.first[3]}, r(s.r), m(s.m), off(s.off), left(units)
     {
-        if (left > 0)
-            q = request(p, r);
     }
     // the next segment: tiles [t0, t1) of item (r, m); nt == 0 (t0 == t1) is an item that sees nothing
     __device__ bool next()
@@ -167,7 +168,16 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
 }
 
 // Unit cut: block c's first unit.
-__device__ __forceinline__ long long cut(long long total, int c, int g) { return total * c / g; }
+__device__ __forceinline__ long long cut(long long total, int c, int g)
+{
+    return total < (1 << 20) ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)g) : total * c / g;  // c < 4096
+}
+
+// How many blocks share the units.
+__device__ __forceinline__ int sharing(long long total, int blocks)
+{
+    return (int)max(1ll, min(total / kMinUnits, (long long)blocks));
+}
 
 template <Rows ROWS, int NK, int R>
 __global__ void __launch_bounds__(kThreadsOf<ROWS>, 1)
@@ -209,12 +219,20 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
     // ---- where this block's units begin: prefix sums of items over requests (in the space of the tiles), then of
     // units over equal stretches of items, a stretch a thread
     int *items = reinterpret_cast<int *>(base);
+    Request *kept = reinterpret_cast<Request *>(base + ((kMaxRequests + 4) & ~3) * sizeof(int));
+    auto fact = [&](int r) { return r < kKept ? kept[r] : request(p, r); };
     {
         int run = 0;
         int *warp_sum = reinterpret_cast<int *>(s.sums);
         for (int at = 0; at < p.n_req; at += kThreads) {
             const int r = at + tid;
-            const int n = r < p.n_req ? request(p, r).items : 0;
+            int n = 0;
+            if (r < p.n_req) {
+                const Request q = request(p, r);
+                n = q.items;
+                if (r < kKept)
+                    kept[r] = q;
+            }
             int a = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -249,18 +267,18 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 else
                     top = mid;
             }
-            Request q = request(p, r);
+            Request q = fact(r);
             int m = lo - items[r];
             for (int i = lo; i < hi; ++i, ++m) {
                 while (m >= q.items) {
-                    q = request(p, ++r);
+                    q = fact(++r);
                     m = 0;
                 }
-                visit(r, m, item_tiles<R>(p, q, m) + 1);
+                visit(r, m, q, item_tiles<R>(p, q, m) + 1);
             }
         };
         long long mine = 0;
-        walk([&](int, int, int units) { mine += units; });
+        walk([&](int, int, const Request &, int units) { mine += units; });
         long long a = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -277,16 +295,19 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             total += s.sums[i];
         }
         const long long first = before + a - mine;
-        long long g = total / plan.min_units;
-        g = max(1ll, min(g, (long long)plan.blocks));
-        const long long from = cut(total, blockIdx.x, (int)g);
+        const int g = sharing(total, plan.blocks);
+        const long long from = cut(total, blockIdx.x, g);
         if (blockIdx.x < g && from >= first && from < first + mine) {
             long long at = first;
-            walk([&](int r, int m, int units) {
+            walk([&](int r, int m, const Request &q, int units) {
                 if (from >= at && from < at + units) {
                     s.r = r;
                     s.m = m;
                     s.off = (int)(from - at);
+                    s.first[0] = q.first;
+                    s.first[1] = q.nq;
+                    s.first[2] = q.before;
+                    s.first[3] = q.items;
                 }
                 at += units;
             });
@@ -298,8 +319,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const long long total = s.total;
-    const int g = (int)max(1ll, min(total / plan.min_units, (long long)plan.blocks));
-    const int c = blockIdx.x;
+    const int g = sharing(total, plan.blocks), c = blockIdx.x;
     const long long from = cut(total, c, g), units = c < g ? cut(total, c + 1, g) - from : 0;
     const uint32_t tmem = s.tmem;
     bool ok = true;
@@ -621,8 +641,9 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             }
             __syncwarp();
         };
-        // i: the next tile to score, j <= i the next to multiply, at most kScores behind.  Whichever is ready goes first:
-        // a tile's rows may wait for the product that frees their space.
+        // i: the next tile to score, j <= i the next to multiply, at most kScores behind.  Whichever is ready goes first (a
+        // tile's rows may wait for the product that frees their space), the product of the two: 250 against 248 us for
+        // 608 tokens over 2048 rows of 512 columns, 335 against 305 us for rows of 576.
         int segment = 0, i = 0, i_st = 0, i_ph = 0, j = 0, j_st = 0;
         Walk<R> w(p, s, units);
         while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
@@ -639,8 +660,10 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 bool score = false;
                 uint64_t since = 0;
                 for (uint32_t spins = 1;; ++spins) {
+                    if (may_multiply && __all_sync(~0u, mbar_test(p_bar, p_ph)))
+                        break;
                     score = may_score && __all_sync(~0u, mbar_test(kv_bar, i_ph));
-                    if (score || (may_multiply && __all_sync(~0u, mbar_test(p_bar, p_ph))))
+                    if (score)
                         break;
                     if ((spins & 255u) == 0) {
                         const uint64_t now = __shfl_sync(~0u, global_ns(), 0);
@@ -721,25 +744,25 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     mbar_arrive(smem_addr(&s.q_full));
             }
             if constexpr (ROWS != kTma) {
-                // Groups of eight rows, counted through the block's tiles; the warp takes every eighth.  A lane finds
-                // the place of one row (lane % 8) a turn ahead.
+                // Groups of eight rows, counted through the block's tiles; the warp takes every eighth.  A lane finds the
+                // page of one row (lane % 8) a turn ahead; 8-bit rows are fetched a turn ahead too (twice the registers
+                // would not do for bf16 rows).
                 const int end = visible(p, w.q, last_token(p, w.q, w.item()));
                 const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
                 const int n_groups = (w.t1 - w.t0) * kGroups;
-                auto look_up = [&](int i) -> int64_t {
-                    const int j = w.t0 * R + i * 8 + (lane & 7);
-                    if (i >= n_groups || j >= end)
-                        return -1;
-                    const int page = __ldg(table + j / p.page_size);
-                    return page >= 0 && page < p.n_pages ? (int64_t)page * p.page_size + j % p.page_size : -2;
-                };
-                int i = (lw - tile * kGroups) & (kLoadWarps - 1);
-                int64_t slot = look_up(i);
-                for (; i < n_groups; i += kLoadWarps) {
-                    const int mine = tile + i / kGroups, gr = i % kGroups, st = mine % stages;
-                    const uint32_t missing = __ballot_sync(~0u, slot == -2) & 0xffu;
-                    constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
+                constexpr bool kAhead = ROWS == kBits8;
+                constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
+                auto row_of = [&](int i) { return w.t0 * R + i * 8 + (lane & 7); };
+                auto look_up = [&](int i) { return i < n_groups && row_of(i) < end ? __ldg(table + row_of(i) / p.page_size) : 0; };
+                struct Fetched {
                     uint4 v[kParts][NK];
+                    float scale;
+                    uint32_t missing;
+                };
+                auto fetch = [&](int i, int page, Fetched &f8) {
+                    const bool need = i < n_groups && row_of(i) < end, found = page >= 0 && page < p.n_pages;
+                    const int64_t slot = need && found ? (int64_t)page * p.page_size + row_of(i) % p.page_size : -1;
+                    f8.missing = __ballot_sync(~0u, need && !found) & 0xffu;
 #pragma unroll
                     for (int h = 0; h < kParts; ++h) {
                         const int64_t at = __shfl_sync(~0u, slot, ROWS == kBits8 ? lane >> 2 : (lane >> 3) + 4 * h);
@@ -747,26 +770,28 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                                                             : cache + at * p.cache_stride * 2 + (lane & 7) * 16;
 #pragma unroll
                         for (int ch = 0; ch < NK; ++ch)
-                            v[h][ch] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * (ROWS == kBits8 ? 64 : 128))) : zero4();
+                            f8.v[h][ch] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * (ROWS == kBits8 ? 64 : 128))) : zero4();
                     }
-                    const float sc = ROWS == kBits8 && slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
-                    slot = look_up(i + kLoadWarps);
+                    f8.scale = ROWS == kBits8 && slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
+                };
+                auto put = [&](int i, const Fetched &f8) {
+                    const int mine = tile + i / kGroups, gr = i % kGroups, st = mine % stages;
                     if (mine >= stages) {
                         ok = mbar_wait(smem_addr(&s.kv_empty[st]), (mine / stages - 1) & 1, status);
                         ok = __all_sync(~0u, ok);
                         if (!ok)
-                            break;
+                            return;
                     }
                     uint8_t *dst = kv_mem + st * kTileBytes + gr * kGroupBytes;
                     if constexpr (ROWS == kBits8) {
                         if (lane < 8)
-                            s.scales[st][gr * 8 + lane] = sc;
+                            s.scales[st][gr * 8 + lane] = f8.scale;
                         const int r = lane >> 2, quarter = lane & 3;  // 16 of a chunk's 64 columns
 #pragma unroll
                         for (int ch = 0; ch < NK; ++ch)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
-                                const uint32_t a = u ? v[0][ch].z : v[0][ch].x, e = u ? v[0][ch].w : v[0][ch].y;
+                                const uint32_t a = u ? f8.v[0][ch].z : f8.v[0][ch].x, e = u ? f8.v[0][ch].w : f8.v[0][ch].y;
                                 *reinterpret_cast<uint4 *>(dst + ch * kGroupChunk + r * 128 + (((2 * quarter + u) ^ r) << 4)) =
                                     make_uint4(bf16x2_of_e4m3x2(a & 0xffffu), bf16x2_of_e4m3x2(a >> 16),
                                                bf16x2_of_e4m3x2(e & 0xffffu), bf16x2_of_e4m3x2(e >> 16));
@@ -777,15 +802,38 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                             const int r = (lane >> 3) + 4 * h;
 #pragma unroll
                             for (int ch = 0; ch < NK; ++ch)
-                                *reinterpret_cast<uint4 *>(dst + ch * kGroupChunk + r * 128 + (((lane & 7) ^ r) << 4)) = v[h][ch];
+                                *reinterpret_cast<uint4 *>(dst + ch * kGroupChunk + r * 128 + (((lane & 7) ^ r) << 4)) = f8.v[h][ch];
                         }
                     }
                     if (lane == 0)
-                        s.missing[st][gr] = (uint8_t)missing;
+                        s.missing[st][gr] = (uint8_t)f8.missing;
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&s.kv_full[st]));
+                };
+                int i = (lw - tile * kGroups) & (kLoadWarps - 1);
+                int page = look_up(i);
+                Fetched a, e;
+                if constexpr (kAhead) {
+                    fetch(i, page, a);
+                    page = look_up(i + kLoadWarps);
+                    for (; ok && i < n_groups; i += 2 * kLoadWarps) {
+                        fetch(i + kLoadWarps, page, e);
+                        page = look_up(i + 2 * kLoadWarps);
+                        put(i, a);
+                        if (!ok || i + kLoadWarps >= n_groups)
+                            break;
+                        fetch(i + 2 * kLoadWarps, page, a);
+                        page = look_up(i + 3 * kLoadWarps);
+                        put(i + kLoadWarps, e);
+                    }
+                } else {
+                    for (; ok && i < n_groups; i += kLoadWarps) {
+                        fetch(i, page, a);
+                        page = look_up(i + kLoadWarps);
+                        put(i, a);
+                    }
                 }
                 tile += w.t1 - w.t0;
             }
@@ -800,19 +848,15 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         while (ok && w.next()) {
             const int end = visible(p, w.q, last_token(p, w.q, w.item()));
             const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
-            // lane % 8 finds the place of one of a tile's groups, a tile ahead
-            auto look_up = [&](int t) {
-                const int j = t * R + (lane & 7) * 8;
-                if (t >= w.t1 || (lane & 7) >= kGroups || j >= end)
-                    return none;
-                const int page = __ldg(table + j / p.page_size);
-                return page >= 0 && page < p.n_pages ? (page * p.page_size + j % p.page_size) >> 3 : -1;
-            };
+            // lane % 8 finds the page of one of a tile's groups, a tile ahead
+            auto needed = [&](int t) { return t < w.t1 && (lane & 7) < kGroups && t * R + (lane & 7) * 8 < end; };
+            auto look_up = [&](int t) { return needed(t) ? __ldg(table + (t * R + (lane & 7) * 8) / p.page_size) : 0; };
             int next = look_up(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
                 const int st = tile % stages;
-                const uint32_t missing = __ballot_sync(~0u, next < 0) & 0xffu;
-                const int at = next < 0 ? none : next;
+                const bool need = needed(t), found = next >= 0 && next < p.n_pages;
+                const uint32_t missing = __ballot_sync(~0u, need && !found) & 0xffu;
+                const int at = need && found ? (next * p.page_size + (t * R + (lane & 7) * 8) % p.page_size) >> 3 : none;
                 next = look_up(t + 1);
                 if (tile >= stages) {
                     ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
@@ -928,8 +972,10 @@ constexpr size_t fixed_of(int nk) { return (size_t)(nk + 1) * kQueryChunk + 1024
 constexpr int stages_of(int nk, int rows) { return (int)((kSmemLimit - fixed_of(nk)) / ((size_t)nk * rows * 128)); }
 
 // Rows of a tile: the tensor core wants wide tiles, the loads want three tiles in flight; so 64 where three fit beside
-// the queries, else 48, else (576 columns) 32 in four.
-constexpr int rows_of(int nk) { return stages_of(nk, 64) >= 3 ? 64 : stages_of(nk, 48) >= 3 ? 48 : 32; }
+// the queries, else 48 (512 columns: a decode step of 64 requests 94.6 us against 97.5 with two tiles of 64 rows), else
+// (576 columns) two of 64 (608 tokens over 2048 rows 260 us against 305 with four of 32, which cost the tensor core as
+// much as 40 would).
+constexpr int rows_of(int nk) { return stages_of(nk, 64) < 3 && stages_of(nk, 48) >= 3 ? 48 : 64; }
 
 MmaPlan make_plan(const AttnParams &p, int num_sms)
 {
@@ -941,12 +987,12 @@ MmaPlan make_plan(const AttnParams &p, int num_sms)
     m.smem += (m.p_buffers - 1) * kQueryChunk;
     // the larger copy: the most groups that divide both the tile and the page
     for (m.box_groups = rows / 8; m.box_groups > 1 && (p.page_size % (8 * m.box_groups) || (rows / 8) % m.box_groups); --m.box_groups) {}
-    // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for the offsets of
-    // kMaxRequests requests
-    m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
+    // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for what cuts the work
+    constexpr size_t least = 1024 + (kMaxRequests + 4) * sizeof(int) + kKept * sizeof(Request);
+    static_assert(least > 114 * 1024 && least < kSmemLimit, "");
+    m.smem = m.smem < least ? least : m.smem;
     m.tmem_columns = p.v_dim > 256 ? 512 : 256;  // O below, the S tiles above
     m.blocks = num_sms;
-    m.min_units = 4;
     return m;
 }
 
