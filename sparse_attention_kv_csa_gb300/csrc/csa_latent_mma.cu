@@ -106,10 +106,10 @@ __device__ __forceinline__ int visible(const AttnParams &p, const Request &q, in
     return held <= 0 ? 0 : min(held / p.ratio, p.width * p.page_size);
 }
 
+// (all in 32 bits: a 64-bit division takes some 500 cycles, and the tokens times the heads stay below 2^31)
 __device__ __forceinline__ int last_token(const AttnParams &p, const Request &q, int m)
 {
-    const int64_t row = min((int64_t)(m + 1) * kTile, (int64_t)q.nq * p.n_heads) - 1;
-    return (int)(row / p.n_heads);
+    return (int)((min((uint32_t)(m + 1) * kTile, (uint32_t)q.nq * (uint32_t)p.n_heads) - 1) / (uint32_t)p.n_heads);
 }
 
 template <int R> __device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
@@ -155,6 +155,21 @@ template <int R> struct Walk {
 };
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
+
+// Read-only loads that stay where they are written: ahead of the waits that they are to overlap.
+__device__ __forceinline__ uint4 load_now(const uint8_t *at)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
+
+__device__ __forceinline__ int load_now(const int32_t *at)
+{
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(at));
+    return v;
+}
 
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t w)
 {
@@ -347,15 +362,26 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 return row < item_rows ? visible(p, w.q, (w.item() * kTile + row) / p.n_heads) : 0;
             };
             const int seen0 = seen_by(r0), seen1 = seen_by(r0 + 8);
-            const int all_see = visible(p, w.q, (int)((int64_t)w.item() * kTile / p.n_heads));
+            const int all_see = visible(p, w.q, (int)((uint32_t)w.item() * kTile / (uint32_t)p.n_heads));
             const int end = visible(p, w.q, last_token(p, w.q, w.item()));
             const bool whole = item_rows == kTile;
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // l: this thread's columns only
             for (int t = w.t0; t < w.t1 && ok; ++t, ++tile) {
                 const int st = tile % stages, b = tile & 1, sb = tile % kScores;
-                // (the loaders' own barrier too: their scales and flags are read below)
-                ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status) &&
-                     mbar_wait(smem_addr(&s.s_full[sb]), (tile / kScores) & 1, status);
+                // (the loaders' own barrier too, for their scales and flags)
+                ok = mbar_wait(smem_addr(&s.kv_full[st]), (tile / stages) & 1, status);
+                const uint64_t missing = *reinterpret_cast<const volatile uint64_t *>(s.missing[st]);
+                float2 rs[R / 8];
+                auto read_scales = [&] {
+#pragma unroll
+                    for (int g8 = 0; g8 < R / 8; ++g8) {
+                        const volatile float *at = &s.scales[st][8 * g8 + cq];
+                        rs[g8] = make_float2(at[0], at[1]);
+                    }
+                };
+                if constexpr (ROWS == kBits8)
+                    read_scales();
+                ok = ok && mbar_wait(smem_addr(&s.s_full[sb]), (tile / kScores) & 1, status);
                 ok = __all_sync(~0u, ok);
                 if (!ok)
                     break;
@@ -367,20 +393,11 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     tmem_ld_16x256(my_lanes + (16u << 16) + sb * 64 + 32 * i, x + 16 * i);
                 if constexpr (R % 32 == 16)
                     tmem_ld_16x256_half(my_lanes + (16u << 16) + sb * 64 + R - 16, x + N - 8);
-                const uint64_t missing = *reinterpret_cast<const volatile uint64_t *>(s.missing[st]);
-                float2 rs[R / 8];
-                if constexpr (ROWS == kBits8) {
-#pragma unroll
-                    for (int g8 = 0; g8 < R / 8; ++g8)
-                        rs[g8] = *reinterpret_cast<const float2 *>(&s.scales[st][8 * g8 + cq]);
-                }
                 tmem_wait_ld();
-                if constexpr (ROWS == kBits8) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        x[i] *= (i & 1) ? rs[i / 4].y : rs[i / 4].x;
-                }
-                if (!whole || (t + 1) * R > all_see || missing) {
+                auto times_scales = [&](float2 v, int i) { return ROWS == kBits8 ? mul2(v, rs[i / 2]) : v; };  // v: x[2 i], x[2 i + 1]
+                const bool masked = !whole || (t + 1) * R > all_see || missing;
+                uint64_t see0 = ~0ull, see1 = ~0ull, poison = 0;
+                if (masked) {
                     if (ROWS == kTma && (t + 1) * R > end) {
                         // Whole groups were copied: rows that no query sees may hold anything, and a weight of zero
                         // does not clear an infinity or NaN of theirs.
@@ -390,7 +407,6 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                                                        (row & 7) * 128 + (unit16 & 7) * 16) = zero4();
                         }
                     }
-                    uint64_t poison = 0;
                     if (all_see < end && (t + 1) * R > all_see) {
                         // Rows that some queries see and some do not: a weight of zero times an infinity or NaN would
                         // reach the queries that do not, so such a row is cleared, and the queries that see it get NaN.
@@ -404,12 +420,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                                     const uint4 v = *reinterpret_cast<const uint4 *>(mem + ch * kGroupChunk + u * 16);
                                     bad |= nonfinite_bf16(v.x) || nonfinite_bf16(v.y) || nonfinite_bf16(v.z) || nonfinite_bf16(v.w);
                                 }
+                        if (ROWS == kBits8 && row < R)
+                            bad |= !isfinite(s.scales[st][row]);
                         const uint32_t lanes = __ballot_sync(~0u, bad);
-                        if (lanes >> (lane & ~1) & 3u)
+                        if (lanes >> (lane & ~1) & 3u) {
                             for (int ch = 0; ch < NK; ++ch)
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
                                     *reinterpret_cast<uint4 *>(mem + ch * kGroupChunk + u * 16) = zero4();
+                            if (ROWS == kBits8)
+                                s.scales[st][row] = 0.0f;
+                        }
                         uint32_t bits = 0;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -425,12 +446,23 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                             break;
                         poison = *reinterpret_cast<const volatile uint64_t *>(s.poison[flagged & 1]) >> cq;
                         ++flagged;
+                        if constexpr (ROWS == kBits8)
+                            read_scales();
                     }
                     auto mask = [&](int seen) {
                         const int lim = seen - t * R;
                         return (~missing & (lim <= 0 ? 0ull : lim >= 64 ? ~0ull : (1ull << lim) - 1)) >> cq;
                     };
-                    const uint64_t see0 = mask(seen0), see1 = mask(seen1);
+                    see0 = mask(seen0);
+                    see1 = mask(seen1);
+                }
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float2 v = times_scales(make_float2(x[2 * i], x[2 * i + 1]), i);
+                    x[2 * i] = v.x;
+                    x[2 * i + 1] = v.y;
+                }
+                if (masked)
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         const int bit = 8 * (i / 4) + (i & 1);
@@ -439,7 +471,6 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         if (!(((i & 2) ? see1 : see0) >> bit & 1))
                             x[i] = -INFINITY;
                     }
-                }
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < N; i += 4) {
@@ -490,12 +521,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         sum1 = add2(sum1, e);
                     else
                         sum0 = add2(sum0, e);
-                    if constexpr (ROWS == kBits8) {
-                        // a hidden row's scale may be anything: its weight stays 0
-                        e.x = e.x == 0.0f ? 0.0f : e.x * rs[i / 2].x;
-                        e.y = e.y == 0.0f ? 0.0f : e.y * rs[i / 2].y;
-                    }
-                    pk[i] = f2_to_bf16x2(e);
+                    // (the scale of a row that the query does not see is finite: its weight stays 0)
+                    pk[i] = f2_to_bf16x2(times_scales(e, i));
                 }
                 l0 += sum0.x + sum0.y;
                 l1 += sum1.x + sum1.y;
@@ -721,7 +748,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                                 (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
 #pragma unroll
                     for (int ch = 0; ch < NK; ++ch)
-                        v[i][ch] = row < item_rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch * 128)) : zero4();
+                        v[i][ch] = row < item_rows ? load_now(src + ch * 128) : zero4();
                 }
                 if (segment > 0) {
                     ok = mbar_wait(smem_addr(&s.q_empty), (segment - 1) & 1, status);
@@ -753,7 +780,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 constexpr bool kAhead = ROWS == kBits8;
                 constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
                 auto row_of = [&](int i) { return w.t0 * R + i * 8 + (lane & 7); };
-                auto look_up = [&](int i) { return i < n_groups && row_of(i) < end ? __ldg(table + row_of(i) / p.page_size) : 0; };
+                auto look_up = [&](int i) { return i < n_groups && row_of(i) < end ? load_now(table + row_of(i) / p.page_size) : 0; };
                 struct Fetched {
                     uint4 v[kParts][NK];
                     float scale;
@@ -770,7 +797,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                                                             : cache + at * p.cache_stride * 2 + (lane & 7) * 16;
 #pragma unroll
                         for (int ch = 0; ch < NK; ++ch)
-                            f8.v[h][ch] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + ch * (ROWS == kBits8 ? 64 : 128))) : zero4();
+                            f8.v[h][ch] = at >= 0 ? load_now(src + ch * (ROWS == kBits8 ? 64 : 128)) : zero4();
                     }
                     f8.scale = ROWS == kBits8 && slot >= 0 ? __ldg(p.row_scales + slot) : 0.0f;
                 };
@@ -850,7 +877,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
             // lane % 8 finds the page of one of a tile's groups, a tile ahead
             auto needed = [&](int t) { return t < w.t1 && (lane & 7) < kGroups && t * R + (lane & 7) * 8 < end; };
-            auto look_up = [&](int t) { return needed(t) ? __ldg(table + (t * R + (lane & 7) * 8) / p.page_size) : 0; };
+            auto look_up = [&](int t) { return needed(t) ? load_now(table + (t * R + (lane & 7) * 8) / p.page_size) : 0; };
             int next = look_up(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
                 const int st = tile % stages;

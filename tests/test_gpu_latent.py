@@ -247,3 +247,14 @@ def test_items_in_a_row_with_few_live_rows():
         for _ in range(5):
             o2, l2 = csa.latent_attention(**a)
             assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_scales_of_later_rows_may_hold_anything():
+    # as test_later_rows...: a row that only later tokens see has a scale of NaN or infinity
+    for bad in (float("nan"), float("inf")):
+        a = made([130], [4], 8, 512, 1, 64, True, seed=8)
+        out, lse = check(a)
+        a["row_scales"][a["block_table"][0, 2], 0] = bad  # row 128
+        out2, lse2 = csa.latent_attention(**a)
+        assert torch.equal(out[:2], out2[:2]) and torch.equal(lse[:2], lse2[:2])
+        assert not out2[2:].isfinite().all()
