@@ -12,7 +12,6 @@ device; ValueError / TypeError name an argument that does not fit, CSAError a ca
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 __all__ = ["csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention", "rms_norm_forward",
@@ -20,6 +19,9 @@ __all__ = ["csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_laten
 
 _lib = None
 _raise = None
+_torch = None
+_Tensor = None
+_raw_stream = None
 
 BF16, F16, F32, E4M3 = 0, 1, 2, 3
 _CODES = {}
@@ -39,23 +41,36 @@ def _bind(lib, check):
     _lib, _raise = lib, check
 
 
+def _load_torch():
+    """torch is imported on first use, like in the rest of the package."""
+    global _torch, _Tensor, _raw_stream
+    import torch
+    _torch, _Tensor = torch, torch.Tensor
+    # the current stream's handle without building a Stream object (some 3 us of a call of 10)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _CODES.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32, torch.float8_e4m3fn: E4M3})
+
+
 def _addr(x):
     return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _torch is None:
+            _load_torch()
+        if _raw_stream is not None:
+            return _raw_stream(_torch.cuda.current_device())
+        return _torch.cuda.current_stream().cuda_stream
     return s if isinstance(s, int) else s.cuda_stream
 
 
-def _on(stream):
-    """Outputs are allocated on the stream that writes them."""
+def _empty(shape, dtype, device, stream):
+    """An output, allocated on the stream that writes it."""
     if stream is None:
-        return contextlib.nullcontext()
-    import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 # ------------------------------------------------------------ the C entry points
@@ -92,40 +107,83 @@ def csa_latent_attention(q, q_token_stride, q_head_stride, cu_q, n_req, n_tokens
 
 # ------------------------------------------------------------ checks
 
-def _codes():
-    if not _CODES:
-        import torch
-        _CODES.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32, torch.float8_e4m3fn: E4M3})
-    return _CODES
-
-
-def _check(name, t, dtype, shape=None, like=None, contiguous=True):
-    """t is a tensor of dtype and shape (None: any extent) on like's device."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a tensor" % name)
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise ValueError("%s must have shape %s (got %s)" % (name, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
-    if like is not None and t.device != like.device:
-        raise ValueError("%s must be on %s (got %s)" % (name, like.device, t.device))
-    if contiguous and not t.is_contiguous():
+def _check(name, t, dtype, shape, device):
+    """t is a contiguous tensor of dtype and shape (None: any extent) on the device (its number, None: any)."""
+    if (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (device is None or t.get_device() == device)):
+        return
+    _fits(name, t, dtype, shape, device)
+    if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
+def _fits(name, t, dtype, shape, device):
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple("*" if w is None else w for w in shape), tuple(t.shape)))
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s must be on cuda:%d (got %s)" % (name, device, t.device))
+
+
 def _check_device(t, name):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    """The number of t's device, which is the current one."""
+    d = t.get_device()
+    if d < 0 or d != _torch.cuda.current_device():
         raise ValueError("%s must be on the current CUDA device (got %s)" % (name, t.device))
+    return d
 
 
-def _rows(name, t, dtype, shape, like):
+def _rows(name, t, dtype, shape, device):
     """A matrix whose rows are contiguous: checked; returns its row stride."""
-    _check(name, t, dtype, shape, like, contiguous=False)
+    if type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return shape[1]
+    _fits(name, t, dtype, shape, device)
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("%s's last dimension must be contiguous" % name)
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(name, t, dtype, device):
+    """t's length: a contiguous vector of dtype on the device."""
+    if type(t) is _Tensor and t.dtype is dtype and t.dim() == 1 and t.is_contiguous() and t.get_device() == device:
+        return t.shape[0]
+    _check(name, t, dtype, (None,), device)
+    return t.shape[0]
+
+
+def _table(name, t, rows, device):
+    """The row stride and width of an int32 matrix of so many rows."""
+    if type(t) is _Tensor and t.dtype is _torch.int32 and t.dim() == 2 and t.is_contiguous() and t.get_device() == device:
+        n, width = t.shape
+        if n == rows:
+            return width, width
+    _fits(name, t, _torch.int32, (rows, None), device)
+    return _rows(name, t, _torch.int32, tuple(t.shape), device), t.shape[1]
+
+
+def _handle(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(name, t):
+    """t's shape, code and device: a matrix in bf16, f16 or f32 on the current device."""
+    if _torch is None:
+        _load_torch()
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    code = _CODES.get(t.dtype, E4M3)
+    if code == E4M3 or t.dim() != 2:
+        raise ValueError("%s must be [n_rows, dim] in bf16, f16 or f32 (got %s, %s)" % (name, tuple(t.shape), t.dtype))
+    return t.shape, code, _check_device(t, name)
 
 
 # ------------------------------------------------------------ helpers
@@ -138,48 +196,45 @@ def rms_norm_forward(x, weight=None, eps=1e-6, residual=None, out_dtype=None, sc
     (int64 [n_rows], needs ``out`` and for 8 bits ``scales``): row i goes to out[slots[i]], nowhere when negative.
     Returns (out, scales or None, x + residual or None, rstd fp32 [n_rows]).
     """
-    import torch
-    codes = _codes()
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a tensor")
-    if x.dim() != 2 or x.dtype not in codes or x.dtype == torch.float8_e4m3fn:
-        raise ValueError("x must be [n_rows, dim] in bf16, f16 or f32 (got %s, %s)" % (tuple(x.shape), x.dtype))
-    _check_device(x, "x")
-    n, dim = x.shape
-    xs = _rows("x", x, x.dtype, (n, dim), x)
-    rs = 0 if residual is None else _rows("residual", residual, x.dtype, (n, dim), x)
+    shape, code, d = _matrix("x", x)
+    n, dim = shape
+    dtype, device, f32 = x.dtype, x.device, _torch.float32
+    xs = dim if x.is_contiguous() else _rows("x", x, dtype, shape, d)
+    rs = 0 if residual is None else _rows("residual", residual, dtype, shape, d)
     if weight is not None:
-        _check("weight", weight, torch.float32, (dim,), x)
-    if out is not None:
-        out_dtype = out.dtype if out_dtype is None else out_dtype
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    if out_dtype != x.dtype and out_dtype != torch.float8_e4m3fn:
-        raise ValueError("out_dtype must be %s or torch.float8_e4m3fn (got %s)" % (x.dtype, out_dtype))
-    bits8 = out_dtype == torch.float8_e4m3fn
-    if scale_group not in (0, 128) or (scale_group and (dim % 128 or not bits8)):
+        _check("weight", weight, f32, (dim,), d)
+    if out_dtype is None:
+        out_dtype = dtype if out is None else out.dtype
+    bits8 = out_dtype == _torch.float8_e4m3fn
+    if out_dtype != dtype and not bits8:
+        raise ValueError("out_dtype must be %s or torch.float8_e4m3fn (got %s)" % (dtype, out_dtype))
+    if scale_group and (scale_group != 128 or dim % 128 or not bits8):
         raise ValueError("scale_group must be 0, or 128 for an 8-bit output of a width that it divides (got %s)" % (scale_group,))
     groups = dim // scale_group if scale_group else 1
     if slots is not None:
-        _check("slots", slots, torch.int64, (n,), x)
+        _check("slots", slots, _torch.int64, (n,), d)
         if out is None or (bits8 and scales is None):
             raise ValueError("slots need out (and scales for an 8-bit output)")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((n, dim), dtype=out_dtype, device=x.device)
-        os_ = _rows("out", out, out_dtype, (n if slots is None else None, dim), x)
-        if bits8:
-            if scales is None:
-                scales = torch.empty((n, groups), dtype=torch.float32, device=x.device)
-            if scales.dim() == 1 and groups == 1:
-                _check("scales", scales, torch.float32, (out.shape[0],), x)
-            else:
-                _check("scales", scales, torch.float32, (out.shape[0], groups), x)
-        elif scales is not None:
-            raise ValueError("scales go with an 8-bit output")
-        total = None if residual is None else torch.empty((n, dim), dtype=x.dtype, device=x.device)
-        rstd = torch.empty((n,), dtype=torch.float32, device=x.device)
-    csa_rms_norm_fwd(x, xs, residual, rs, weight, n, dim, eps, codes[x.dtype], slots, out.shape[0], out, os_,
-                     codes[out_dtype], scales, scale_group, total, rstd, stream)
+    if out is None:
+        out, out_stride = _empty(shape, out_dtype, device, stream), dim
+    else:
+        out_stride = _rows("out", out, out_dtype, (n if slots is None else None, dim), d)
+    if bits8:
+        if scales is None:
+            scales = _empty((n, groups), f32, device, stream)
+        elif groups == 1 and isinstance(scales, _torch.Tensor) and scales.dim() == 1:
+            _check("scales", scales, f32, (out.shape[0],), d)
+        else:
+            _check("scales", scales, f32, (out.shape[0], groups), d)
+    elif scales is not None:
+        raise ValueError("scales go with an 8-bit output")
+    total = None if residual is None else _empty(shape, dtype, device, stream)
+    rstd = _empty((n,), f32, device, stream)
+    rc = _lib.csa_rms_norm_fwd(x.data_ptr(), xs, _pointer(residual), rs, _pointer(weight), n, dim, eps, code, _pointer(slots),
+                               out.shape[0], out.data_ptr(), out_stride, E4M3 if bits8 else code, _pointer(scales),
+                               scale_group, _pointer(total), rstd.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
     return out, scales, total, rstd
 
 
@@ -189,24 +244,21 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, stream=None
     h is the forward's x + residual (x without a residual), rstd its fourth result; grad_residual the gradient that
     reaches x + residual directly.
     """
-    import torch
-    codes = _codes()
-    if not isinstance(h, torch.Tensor):
-        raise TypeError("h must be a tensor")
-    if h.dim() != 2 or h.dtype not in codes or h.dtype == torch.float8_e4m3fn:
-        raise ValueError("h must be [n_rows, dim] in bf16, f16 or f32 (got %s, %s)" % (tuple(h.shape), h.dtype))
-    _check_device(h, "h")
-    n, dim = h.shape
-    hs = _rows("h", h, h.dtype, (n, dim), h)
-    gs = _rows("grad_out", grad_out, h.dtype, (n, dim), h)
-    rs = 0 if grad_residual is None else _rows("grad_residual", grad_residual, h.dtype, (n, dim), h)
+    shape, code, d = _matrix("h", h)
+    n, dim = shape
+    dtype, device, f32 = h.dtype, h.device, _torch.float32
+    hs = dim if h.is_contiguous() else _rows("h", h, dtype, shape, d)
+    gs = _rows("grad_out", grad_out, dtype, shape, d)
+    rs = 0 if grad_residual is None else _rows("grad_residual", grad_residual, dtype, shape, d)
     if weight is not None:
-        _check("weight", weight, torch.float32, (dim,), h)
-    _check("rstd", rstd, torch.float32, (n,), h)
-    with _on(stream):
-        grad_x = torch.empty((n, dim), dtype=h.dtype, device=h.device)
-        grad_weight = torch.empty((dim,), dtype=torch.float32, device=h.device)
-    csa_rms_norm_bwd(h, hs, grad_out, gs, grad_residual, rs, weight, rstd, n, dim, codes[h.dtype], grad_x, grad_weight, stream)
+        _check("weight", weight, f32, (dim,), d)
+    _check("rstd", rstd, f32, (n,), d)
+    grad_x = _empty(shape, dtype, device, stream)
+    grad_weight = _empty((dim,), f32, device, stream)
+    rc = _lib.csa_rms_norm_bwd(h.data_ptr(), hs, grad_out.data_ptr(), gs, _pointer(grad_residual), rs, _pointer(weight),
+                               rstd.data_ptr(), n, dim, code, grad_x.data_ptr(), grad_weight.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
     return grad_x, grad_weight
 
 
@@ -219,29 +271,32 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
     Returns (table, cu_rows int32 [n_req + 1], slots int64 [capacity], counts int32 [4]: new rows, pages taken, pages
     short, pages of the widest request).
     """
-    import torch
-    i32 = torch.int32
-    _check("before", before, i32, (None,))
-    n = before.shape[0]
-    _check_device(before, "before")
-    _check("after", after, i32, (n,), before)
-    _check("free_pages", free_pages, i32, (None,), before)
+    if _torch is None:
+        _load_torch()
+    i32 = _torch.int32
+    if not isinstance(before, _torch.Tensor):
+        raise TypeError("before must be a tensor")
+    d, device = _check_device(before, "before"), before.device
+    n = _vector("before", before, i32, d)
+    _check("after", after, i32, (n,), d)
+    n_free = _vector("free_pages", free_pages, i32, d)
     if taken is not None:
-        _check("taken", taken, i32, (1,), before)
-    stride = _rows("block_table", block_table, i32, (n, None), before)
-    width = block_table.shape[1]
+        _check("taken", taken, i32, (1,), d)
+    stride, width = _table("block_table", block_table, n, d)
     if capacity < 0:
         raise ValueError("capacity must be >= 0 (got %s)" % (capacity,))
-    with _on(stream):
-        if out is None:
-            out = torch.empty((n, width), dtype=i32, device=before.device)
-        else:
-            _check("out", out, i32, (n, width), before)
-        cu_rows = torch.empty((n + 1,), dtype=i32, device=before.device)
-        slots = torch.empty((capacity,), dtype=torch.int64, device=before.device)
-        counts = torch.empty((4,), dtype=i32, device=before.device)
-    csa_page_tables(before, after, n, ratio, page_size, free_pages, free_pages.shape[0], taken, block_table, stride, width,
-                    capacity, out, cu_rows, slots, counts, stream)
+    if out is None:
+        out = _empty((n, width), i32, device, stream)
+    else:
+        _check("out", out, i32, (n, width), d)
+    cu_rows = _empty((n + 1,), i32, device, stream)
+    slots = _empty((capacity,), _torch.int64, device, stream)
+    counts = _empty((4,), i32, device, stream)
+    rc = _lib.csa_page_tables(before.data_ptr(), after.data_ptr(), n, ratio, page_size, free_pages.data_ptr(), n_free,
+                              _pointer(taken), block_table.data_ptr(), stride, width, capacity, out.data_ptr(),
+                              cu_rows.data_ptr(), slots.data_ptr(), counts.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
     return out, cu_rows, slots, counts
 
 
@@ -254,45 +309,54 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
     ratio: tokens a row; v_dim: leading columns that are the values (all by default); sink fp32 [n_heads] or None.
     Returns (out bf16 [n_tokens, n_heads, v_dim], lse fp32 [n_tokens, n_heads]); see csa_latent_attention.
     """
-    import torch
-    _check("q", q, torch.bfloat16, (None, None, None), contiguous=False)
-    _check_device(q, "q")
+    if _torch is None:
+        _load_torch()
+    bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
+    if type(q) is not _Tensor or q.dtype is not bf16 or q.dim() != 3:
+        _fits("q", q, bf16, (None, None, None), None)
+    d, device = _check_device(q, "q"), q.device
     n, heads, dim = q.shape
-    if q.stride(2) != 1 and dim > 1:
+    q_token, q_head, q_column = q.stride()
+    if q_column != 1 and dim > 1:
         raise ValueError("q's last dimension must be contiguous")
-    if not isinstance(cache, torch.Tensor):
+    if not isinstance(cache, _torch.Tensor):
         raise TypeError("cache must be a tensor")
-    bits8 = cache.dtype == torch.float8_e4m3fn
-    if not bits8 and cache.dtype != torch.bfloat16:
+    bits8 = cache.dtype == _torch.float8_e4m3fn
+    if not bits8 and cache.dtype != bf16:
         raise ValueError("cache must be bf16 or float8_e4m3fn (got %s)" % cache.dtype)
-    _check("cache", cache, cache.dtype, (None, None, dim), q, contiguous=False)
-    pages, page_size = cache.shape[0], cache.shape[1]
+    if cache.dim() != 3 or cache.shape[2] != dim or cache.get_device() != d:
+        _fits("cache", cache, cache.dtype, (None, None, dim), d)
+    pages, page_size, _ = cache.shape
     if page_size < 1:
         raise ValueError("cache must have at least one row a page")
-    row = cache.stride(1) if page_size > 1 else cache.stride(0) if pages > 1 else dim
-    if cache.numel() and (cache.stride(2) != 1 or (pages > 1 and cache.stride(0) != row * page_size)):
-        raise ValueError("cache's rows must be contiguous and evenly spaced")
+    if cache.is_contiguous():
+        row = dim
+    else:
+        row = cache.stride(1) if page_size > 1 else cache.stride(0) if pages > 1 else dim
+        if cache.stride(2) != 1 or (pages > 1 and cache.stride(0) != row * page_size):
+            raise ValueError("cache's rows must be contiguous and evenly spaced")
     if bits8 != (row_scales is not None):
         raise ValueError("row_scales go with a float8_e4m3fn cache, and it with them")
     if bits8:
-        _check("row_scales", row_scales, torch.float32, (pages, page_size), q)
-    _check("cu_q", cu_q, torch.int32, (None,), q)
-    n_req = cu_q.shape[0] - 1
+        _check("row_scales", row_scales, f32, (pages, page_size), d)
+    n_req = _vector("cu_q", cu_q, i32, d) - 1
     if n_req < 0:
         raise ValueError("cu_q must be [n_req + 1]")
-    _check("seq_lens", seq_lens, torch.int32, (n_req,), q)
-    stride = _rows("block_table", block_table, torch.int32, (n_req, None), q)
+    _check("seq_lens", seq_lens, i32, (n_req,), d)
+    stride, width = _table("block_table", block_table, n_req, d)
     if sink is not None:
-        _check("sink", sink, torch.float32, (heads,), q)
+        _check("sink", sink, f32, (heads,), d)
     v_dim = dim if v_dim is None else v_dim
-    with _on(stream):
-        if out is None:
-            out = torch.empty((n, heads, v_dim), dtype=torch.bfloat16, device=q.device)
-        else:
-            _check("out", out, torch.bfloat16, (n, heads, v_dim), q)
-        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
-    csa_latent_attention(q, q.stride(0) if n > 1 else max(q.stride(0), dim), q.stride(1) if heads > 1 else max(q.stride(1), dim),
-                         cu_q, n_req, n, heads, dim, v_dim, cache, row, E4M3 if bits8 else BF16, row_scales, pages,
-                         page_size, block_table, stride, block_table.shape[1], seq_lens, ratio, scale, sink, out, lse,
-                         stream)
+    if out is None:
+        out = _empty((n, heads, v_dim), bf16, device, stream)
+    else:
+        _check("out", out, bf16, (n, heads, v_dim), d)
+    lse = _empty((n, heads), f32, device, stream)
+    rc = _lib.csa_latent_attention(q.data_ptr(), q_token if n > 1 else max(q_token, dim), q_head if heads > 1 else max(q_head, dim),
+                                   cu_q.data_ptr(), n_req, n, heads, dim, v_dim, cache.data_ptr(), row,
+                                   E4M3 if bits8 else BF16, _pointer(row_scales), pages, page_size, block_table.data_ptr(),
+                                   stride, width, seq_lens.data_ptr(), ratio, scale, _pointer(sink), out.data_ptr(),
+                                   lse.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
     return out, lse
