@@ -19,6 +19,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "csa_device.cuh"
 #include "csa_launch.h"
 #include "csa_serving_launch.h"
@@ -48,11 +50,13 @@ template <typename T, int VEC> struct alignas(VEC == 1 ? sizeof(T) : sizeof(T) *
     T v[VEC];
 };
 
+// (volatile: the load stays where it is written, ahead of the barriers that it is to overlap)
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load(const T *p)
 {
     Pack<T, VEC> r;
     if constexpr (VEC * sizeof(T) == 16) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+        uint4 u;
+        asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
         memcpy(&r, &u, 16);
     } else {
         static_assert(VEC == 1, "a vector is 16 bytes");
@@ -64,6 +68,52 @@ template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load(cons
 template <typename T, int VEC> __device__ __forceinline__ void store(T *p, const Pack<T, VEC> &v)
 {
     *reinterpret_cast<Pack<T, VEC> *>(p) = v;
+}
+
+// A pack's values in fp32 and back (one rounding each), in pairs where the type has them.
+template <typename T, int VEC> __device__ __forceinline__ void unpack(const Pack<T, VEC> &a, float (&v)[VEC])
+{
+    if constexpr (sizeof(T) == 2 && VEC > 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            uint32_t w;
+            memcpy(&w, &a.v[k], 4);
+            float2 f;
+            if constexpr (std::is_same<T, __half>::value)
+                f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            else
+                f = bf16x2_to_f2(w);
+            v[k] = f.x;
+            v[k + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            v[k] = Elem<T>::to(a.v[k]);
+    }
+}
+
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> pack(const float (&v)[VEC])
+{
+    Pack<T, VEC> a;
+    if constexpr (sizeof(T) == 2 && VEC > 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            uint32_t w;
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(v[k], v[k + 1]);
+                memcpy(&w, &h, 4);
+            } else {
+                w = f2_to_bf16x2(make_float2(v[k], v[k + 1]));
+            }
+            memcpy(&a.v[k], &w, 4);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            a.v[k] = Elem<T>::from(v[k]);
+    }
+    return a;
 }
 
 // Sum (or NaN-propagating maximum of magnitudes) over a team of TEAM threads, the same value and order in every
@@ -137,17 +187,21 @@ norm_fwd_kernel(const NormFwdParams p)
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + t) * VEC;
             if (live && c < p.dim) {
-                Pack<T, VEC> hp;
+                unpack(nx[i], h[i]);
+                if (res) {
+                    float r[VEC];
+                    unpack(nr[i], r);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    hp.v[k] = nx[i].v[k];
-                    if (res)
-                        hp.v[k] = Elem<T>::from(Elem<T>::to(nx[i].v[k]) + Elem<T>::to(nr[i].v[k]));
-                    h[i][k] = Elem<T>::to(hp.v[k]);
-                    ss = fmaf(h[i][k], h[i][k], ss);
+                    for (int k = 0; k < VEC; ++k)
+                        r[k] += h[i][k];
+                    const Pack<T, VEC> hp = pack<T, VEC>(r);
+                    if (p.residual_out)
+                        store<T, VEC>(static_cast<T *>(p.residual_out) + row * p.dim + c, hp);
+                    unpack(hp, h[i]);
                 }
-                if (res && p.residual_out)
-                    store<T, VEC>(static_cast<T *>(p.residual_out) + row * p.dim + c, hp);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    ss = fmaf(h[i][k], h[i][k], ss);
             } else {
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
@@ -180,13 +234,8 @@ norm_fwd_kernel(const NormFwdParams p)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = (i * TEAM + t) * VEC;
-                    if (c < p.dim) {
-                        Pack<OUT, VEC> o;
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k)
-                            o.v[k] = Elem<OUT>::from(h[i][k]);
-                        store<OUT, VEC>(out + c, o);
-                    }
+                    if (c < p.dim)
+                        store<OUT, VEC>(out + c, pack<OUT, VEC>(h[i]));
                 }
         } else {
             // 128 columns lie in 128 / VEC neighbouring lanes; the host takes that form with whole vectors only
@@ -212,10 +261,19 @@ norm_fwd_kernel(const NormFwdParams p)
                 const float inv = scale > 0.0f && !tiny ? 1.0f / scale : 1.0f;
                 if (write && c < p.dim) {
                     Pack<__nv_fp8_storage_t, VEC> o;
+                    if (tiny && scale > 0.0f)
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const float q = tiny && scale > 0.0f ? h[i][k] / scale : h[i][k] * inv;
-                        o.v[k] = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+                        for (int k = 0; k < VEC; ++k)
+                            h[i][k] /= scale;
+                    if constexpr (VEC > 1) {
+#pragma unroll
+                        for (int k = 0; k < VEC; k += 2) {
+                            const __nv_fp8x2_storage_t two =
+                                __nv_cvt_float2_to_fp8x2(make_float2(h[i][k] * inv, h[i][k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                            memcpy(&o.v[k], &two, 2);
+                        }
+                    } else {
+                        o.v[0] = __nv_cvt_float_to_fp8(h[i][0] * inv, __NV_SATFINITE, __NV_E4M3);
                     }
                     store<__nv_fp8_storage_t, VEC>(reinterpret_cast<__nv_fp8_storage_t *>(out) + c, o);
                     if (grouped ? (c & 127) == 0 : c == 0)
@@ -226,12 +284,15 @@ norm_fwd_kernel(const NormFwdParams p)
     }
 }
 
+// Teams of 1024 threads (rows of more than 1024 vectors) have 64 registers a thread: they neither keep the weights nor
+// load a row ahead.
 template <typename T, int VEC, int TEAM, int NV>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM)
 norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
 {
     constexpr int kThreads = TEAM < 256 ? 256 : TEAM;
     constexpr int kTeams = kThreads / TEAM;
+    constexpr bool kRoomy = TEAM < 1024;
     __shared__ float buf[2][kThreads / 32];
     __shared__ float fold[kTeams > 1 ? (kTeams - 1) * TEAM * NV * VEC : 1];
     pdl_wait();
@@ -239,65 +300,93 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
     const T *h = static_cast<const T *>(p.h), *dy = static_cast<const T *>(p.grad_out);
     const T *dh = static_cast<const T *>(p.grad_residual);
+    auto weight_at = [&](int i, int k) {
+        const int c = (i * TEAM + t) * VEC + k;
+        return c < p.dim ? (p.weight ? __ldg(p.weight + c) : 1.0f) : 0.0f;
+    };
     float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            const int c = (i * TEAM + t) * VEC + k;
-            w[i][k] = c < p.dim ? (p.weight ? __ldg(p.weight + c) : 1.0f) : 0.0f;
+            if (kRoomy)
+                w[i][k] = weight_at(i, k);
             dw[i][k] = 0.0f;
         }
     const float inv_dim = 1.0f / (float)p.dim;
     const int64_t step = (int64_t)gridDim.x * kTeams;
     const int64_t passes = (p.n_rows + step - 1) / step;
     int64_t row = (int64_t)blockIdx.x * kTeams + team;
-    for (int64_t it = 0; it < passes; ++it, row += step) {
-        const bool live = row < p.n_rows;
-        Pack<T, VEC> hp[NV], gp[NV], rp[NV];
-        float rstd = 0.0f, sum = 0.0f;
-        if (live) {
-            rstd = __ldg(p.rstd + row);
+    struct Row {
+        Pack<T, VEC> h[NV], g[NV], r[NV];
+        float rstd;
+    };
+    auto fetch = [&](int64_t r, Row &x) {
+        if (r >= p.n_rows)
+            return;
+        x.rstd = __ldg(p.rstd + r);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * TEAM + t) * VEC;
-                if (c < p.dim) {
-                    hp[i] = load<T, VEC>(h + row * p.h_stride + c);
-                    gp[i] = load<T, VEC>(dy + row * p.grad_out_stride + c);
-                    if (dh)
-                        rp[i] = load<T, VEC>(dh + row * p.grad_residual_stride + c);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * TEAM + t) * VEC;
-                if (c < p.dim)
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const float unit = Elem<T>::to(hp[i].v[k]) * rstd, g = Elem<T>::to(gp[i].v[k]);
-                        dw[i][k] = fmaf(g, unit, dw[i][k]);
-                        sum = fmaf(g * w[i][k], unit, sum);
-                    }
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TEAM + t) * VEC;
+            if (c < p.dim) {
+                x.h[i] = load<T, VEC>(h + r * p.h_stride + c);
+                x.g[i] = load<T, VEC>(dy + r * p.grad_out_stride + c);
+                if (dh)
+                    x.r[i] = load<T, VEC>(dh + r * p.grad_residual_stride + c);
             }
         }
-        const float c_mean = team_reduce<TEAM, false>(sum, buf[it & 1]) * inv_dim;
-        if (live)
+    };
+    // unit = h rstd, g = w dy
+    auto values = [&](const Row &x, int i, float (&unit)[VEC], float (&g)[VEC], float (&raw)[VEC]) {
+        unpack(x.h[i], unit);
+        unpack(x.g[i], raw);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * TEAM + t) * VEC;
-                if (c < p.dim) {
-                    Pack<T, VEC> o;
+        for (int k = 0; k < VEC; ++k) {
+            unit[k] *= x.rstd;
+            g[k] = raw[k] * (kRoomy ? w[i][k] : weight_at(i, k));
+        }
+    };
+    Row now, next;
+    if (kRoomy)
+        fetch(row, next);
+    for (int64_t it = 0; it < passes; ++it, row += step) {
+        const bool live = row < p.n_rows;
+        if (kRoomy) {
+            now = next;
+            fetch(row + step, next);
+        } else {
+            fetch(row, now);
+        }
+        float sum = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) {
-                        const float unit = Elem<T>::to(hp[i].v[k]) * rstd, g = Elem<T>::to(gp[i].v[k]);
-                        float d = rstd * fmaf(-unit, c_mean, g * w[i][k]);
-                        if (dh)
-                            d += Elem<T>::to(rp[i].v[k]);
-                        o.v[k] = Elem<T>::from(d);
-                    }
-                    store<T, VEC>(static_cast<T *>(p.grad_x) + row * p.dim + c, o);
+        for (int i = 0; i < NV; ++i)
+            if (live && (i * TEAM + t) * VEC < p.dim) {
+                float unit[VEC], g[VEC], raw[VEC];
+                values(now, i, unit, g, raw);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    dw[i][k] = fmaf(raw[k], unit[k], dw[i][k]);
+                    sum = fmaf(g[k], unit[k], sum);
                 }
             }
+        const float c_mean = team_reduce<TEAM, false>(sum, buf[it & 1]) * inv_dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TEAM + t) * VEC;
+            if (live && c < p.dim) {
+                float unit[VEC], g[VEC], raw[VEC], d[VEC];
+                values(now, i, unit, g, raw);
+                if (dh)
+                    unpack(now.r[i], raw);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    d[k] = now.rstd * fmaf(-unit[k], c_mean, g[k]);
+                    if (dh)
+                        d[k] += raw[k];
+                }
+                store<T, VEC>(static_cast<T *>(p.grad_x) + row * p.dim + c, pack<T, VEC>(d));
+            }
+        }
     }
     if constexpr (kTeams > 1) {
         // the teams' sums of one block, added in ascending team order
