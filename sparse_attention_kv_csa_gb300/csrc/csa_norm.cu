@@ -13,8 +13,10 @@
 //
 // Both are bound by DRAM: every array is read or written once and a row stays in registers between its sums and its
 // output.  A row belongs to one team of 32 to 1024 threads; a block holds one team (or several small ones) and walks
-// the rows with the grid's stride, its weights in registers, the next row's words loaded before the current row's
-// sums are exchanged.  All sums are fp32; h is rounded to T before the norm because that is what the next layer and
+// the rows with the grid's stride, its weights in registers.  Rows of 16-byte vectors for teams of 128 threads or more
+// come by bulk copies into a ring of rows in shared memory, several rows ahead (loads into registers a row ahead kept
+// too few bytes on the way: 130 against 95 us for 16411 rows of 4096 with 8-bit output); other rows are loaded into
+// registers a row ahead.  All sums are fp32; h is rounded to T before the norm because that is what the next layer and
 // the backward read.  dw: one partial row per block, added in a fixed order by a second kernel (no atomics).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -139,6 +141,41 @@ template <int TEAM, bool MAX> __device__ __forceinline__ float team_reduce(float
     return v;
 }
 
+// A ring of rows in shared memory: the arrays' rows side by side, refilled by the block's first thread once the block
+// has read them.
+struct Ring {
+    uint8_t *mem;
+    uint64_t *full;
+    int stages, row_bytes, arrays;
+    unsigned *status;
+    __device__ void init() const
+    {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < stages; ++i)
+                mbar_init(smem_addr(full + i), 1);
+            mbar_init_fence();
+        }
+        __syncthreads();
+    }
+    __device__ void fill(int stage, const void *a, const void *b, const void *c) const
+    {
+        const uint32_t bar = smem_addr(full + stage), dst = smem_addr(mem) + stage * arrays * row_bytes;
+        mbar_arrive_expect_tx(bar, arrays * row_bytes);
+        bulk_g2s(dst, a, row_bytes, bar);
+        if (b)
+            bulk_g2s(dst + row_bytes, b, row_bytes, bar);
+        if (c)
+            bulk_g2s(dst + (arrays - 1) * row_bytes, c, row_bytes, bar);
+    }
+    __device__ const uint8_t *at(int stage, int array) const { return mem + (stage * arrays + array) * row_bytes; }
+};
+constexpr int kMaxRing = 8;
+
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> from_ring(const uint8_t *row, int c)
+{
+    return *reinterpret_cast<const Pack<T, VEC> *>(row + c * sizeof(T));
+}
+
 // Every thread of a block runs the same number of rows (idle teams take no row), so the barriers above are uniform.
 template <typename T, typename OUT, int VEC, int TEAM, int NV>
 __global__ void __launch_bounds__(TEAM < 128 ? 128 : TEAM)
@@ -147,7 +184,13 @@ norm_fwd_kernel(const NormFwdParams p)
     constexpr int kThreads = TEAM < 128 ? 128 : TEAM;
     constexpr int kTeams = kThreads / TEAM;
     constexpr bool kBits8 = sizeof(OUT) == 1;
+    constexpr bool kStaged = VEC > 1 && TEAM >= 128;
     __shared__ float buf[4][kThreads / 32];
+    __shared__ uint64_t full[kMaxRing];
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    const Ring ring{ring_mem, full, p.stages, p.dim * (int)sizeof(T), p.residual ? 2 : 1, p.status};
+    if (kStaged)
+        ring.init();
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
@@ -164,8 +207,12 @@ norm_fwd_kernel(const NormFwdParams p)
     const int64_t step = (int64_t)gridDim.x * kTeams;
     const int64_t passes = (p.n_rows + step - 1) / step;
     Pack<T, VEC> nx[NV], nr[NV];
+    auto refill = [&](int64_t row, int stage) {
+        if (row < p.n_rows)
+            ring.fill(stage, x + row * p.x_stride, res ? res + row * p.residual_stride : nullptr, nullptr);
+    };
     auto fetch = [&](int64_t row) {
-        if (row >= p.n_rows)
+        if (kStaged || row >= p.n_rows)
             return;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -179,10 +226,28 @@ norm_fwd_kernel(const NormFwdParams p)
     };
     int64_t row = (int64_t)blockIdx.x * kTeams + team;
     fetch(row);
+    if (kStaged && threadIdx.x == 0)
+        for (int i = 0; i < ring.stages; ++i)
+            refill(row + i * step, i);
+    int stage = 0;
+    uint32_t phase = 0;
     for (int64_t it = 0; it < passes; ++it, row += step) {
         const bool live = row < p.n_rows;
         float h[NV][VEC];
         float ss = 0.0f;
+        if (kStaged && live) {
+            // (a wait that gives up sets the device's status word; the rows' results are then wrong, as documented)
+            mbar_wait(smem_addr(full + stage), phase, ring.status);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TEAM + t) * VEC;
+                if (c < p.dim) {
+                    nx[i] = from_ring<T, VEC>(ring.at(stage, 0), c);
+                    if (res)
+                        nr[i] = from_ring<T, VEC>(ring.at(stage, 1), c);
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + t) * VEC;
@@ -210,6 +275,15 @@ norm_fwd_kernel(const NormFwdParams p)
         }
         fetch(row + step);
         ss = team_reduce<TEAM, false>(ss, buf[it & 1]);
+        if (kStaged) {
+            // the sum's barrier: the whole block has read the stage
+            if (threadIdx.x == 0)
+                refill(row + ring.stages * step, stage);
+            if (++stage == ring.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
         const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
         int64_t to = row;
         if (live) {
@@ -284,8 +358,7 @@ norm_fwd_kernel(const NormFwdParams p)
     }
 }
 
-// Teams of 1024 threads (rows of more than 1024 vectors) have 64 registers a thread: they neither keep the weights nor
-// load a row ahead.
+// Teams of 1024 threads (rows of more than 1024 vectors) have 64 registers a thread: they do not keep the weights.
 template <typename T, int VEC, int TEAM, int NV>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM)
 norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
@@ -293,6 +366,12 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
     constexpr int kThreads = TEAM < 256 ? 256 : TEAM;
     constexpr int kTeams = kThreads / TEAM;
     constexpr bool kRoomy = TEAM < 1024;
+    constexpr bool kStaged = VEC > 1 && TEAM >= 128 && kTeams == 1;
+    __shared__ uint64_t full[kMaxRing];
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    const Ring ring{ring_mem, full, p.stages, p.dim * (int)sizeof(T), p.grad_residual ? 3 : 2, p.status};
+    if (kStaged)
+        ring.init();
     __shared__ float buf[2][kThreads / 32];
     __shared__ float fold[kTeams > 1 ? (kTeams - 1) * TEAM * NV * VEC : 1];
     pdl_wait();
@@ -347,11 +426,37 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
         }
     };
     Row now, next;
-    if (kRoomy)
+    auto refill = [&](int64_t r, int stage) {
+        if (r < p.n_rows)
+            ring.fill(stage, h + r * p.h_stride, dy + r * p.grad_out_stride, dh ? dh + r * p.grad_residual_stride : nullptr);
+    };
+    if (kStaged) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < ring.stages; ++i)
+                refill(row + i * step, i);
+    } else if (kRoomy) {
         fetch(row, next);
+    }
+    int stage = 0;
+    uint32_t phase = 0;
     for (int64_t it = 0; it < passes; ++it, row += step) {
         const bool live = row < p.n_rows;
-        if (kRoomy) {
+        if (kStaged) {
+            if (live) {
+                now.rstd = __ldg(p.rstd + row);
+                mbar_wait(smem_addr(full + stage), phase, ring.status);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * TEAM + t) * VEC;
+                    if (c < p.dim) {
+                        now.h[i] = from_ring<T, VEC>(ring.at(stage, 0), c);
+                        now.g[i] = from_ring<T, VEC>(ring.at(stage, 1), c);
+                        if (dh)
+                            now.r[i] = from_ring<T, VEC>(ring.at(stage, 2), c);
+                    }
+                }
+            }
+        } else if (kRoomy) {
             now = next;
             fetch(row + step, next);
         } else {
@@ -370,6 +475,14 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
                 }
             }
         const float c_mean = team_reduce<TEAM, false>(sum, buf[it & 1]) * inv_dim;
+        if (kStaged) {
+            if (threadIdx.x == 0)
+                refill(row + ring.stages * step, stage);
+            if (++stage == ring.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + t) * VEC;
@@ -440,9 +553,10 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *__restr
 }
 
 template <typename Kernel, typename... Args>
-cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, cudaStream_t st, Args... args)
+cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.stream = st;
@@ -453,24 +567,37 @@ cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, cudaStream_t st, Args...
 }
 
 // Persistent grid: as many blocks as are resident at once, or fewer where the rows end sooner.
-template <typename Kernel> cudaError_t norm_grid(Kernel k, int threads, int teams, int64_t rows, int *grid)
+template <typename Kernel> cudaError_t norm_grid(Kernel k, int threads, int teams, size_t smem, int64_t rows, int *grid)
 {
     int resident = 0;
-    cudaError_t e = resident_blocks(reinterpret_cast<const void *>(k), threads, 0, 1, &resident);
+    cudaError_t e = resident_blocks(reinterpret_cast<const void *>(k), threads, smem, 1, &resident);
     const int64_t want = (rows + teams - 1) / teams;
     *grid = (int)(want < resident ? want : resident);
     return e;
 }
 
+// Rows in a block's ring: about 64 KB, so that three or four blocks' rings fill an SM's shared memory; one row where
+// two would not fit.
+int ring_stages(int row_bytes, int arrays, int64_t rows)
+{
+    const int bytes = row_bytes * arrays;
+    int n = (64 * 1024) / bytes;
+    n = n > kMaxRing ? kMaxRing : n < 2 && 2 * bytes <= 216 * 1024 ? 2 : n < 1 ? 1 : n;
+    return n > rows ? (int)rows : n;
+}
+
 template <typename T, typename OUT, int VEC, int TEAM, int NV>
-cudaError_t fwd_go(const NormFwdParams &p, cudaStream_t st)
+cudaError_t fwd_go(NormFwdParams p, cudaStream_t st)
 {
     constexpr int threads = TEAM < 128 ? 128 : TEAM;
+    const int arrays = p.residual ? 2 : 1, row_bytes = p.dim * (int)sizeof(T);
+    p.stages = VEC > 1 && TEAM >= 128 ? ring_stages(row_bytes, arrays, p.n_rows) : 0;
+    const size_t smem = (size_t)p.stages * arrays * row_bytes;
     int grid = 0;
-    cudaError_t e = norm_grid(norm_fwd_kernel<T, OUT, VEC, TEAM, NV>, threads, threads / TEAM, p.n_rows, &grid);
+    cudaError_t e = norm_grid(norm_fwd_kernel<T, OUT, VEC, TEAM, NV>, threads, threads / TEAM, smem, p.n_rows, &grid);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(norm_fwd_kernel<T, OUT, VEC, TEAM, NV>, dim3(grid), dim3(threads), st, p);
+    return launch_pdl(norm_fwd_kernel<T, OUT, VEC, TEAM, NV>, dim3(grid), dim3(threads), smem, st, p);
 }
 
 // A row of `words` vectors (or elements) goes to the smallest team whose threads hold at most four vectors (sixteen
@@ -495,15 +622,18 @@ template <typename T, typename OUT> cudaError_t fwd_size(const NormFwdParams &p,
 }
 
 template <typename T, int VEC, int TEAM, int NV>
-cudaError_t bwd_go(const NormBwdParams &p, float *partial, int *blocks, bool plan, cudaStream_t st)
+cudaError_t bwd_go(NormBwdParams p, float *partial, int *blocks, bool plan, cudaStream_t st)
 {
     constexpr int threads = TEAM < 256 ? 256 : TEAM;
+    const int arrays = p.grad_residual ? 3 : 2, row_bytes = p.dim * (int)sizeof(T);
+    p.stages = VEC > 1 && threads == TEAM ? ring_stages(row_bytes, arrays, p.n_rows) : 0;
+    const size_t smem = (size_t)p.stages * arrays * row_bytes;
     int grid = 0;
-    cudaError_t e = norm_grid(norm_bwd_kernel<T, VEC, TEAM, NV>, threads, threads / TEAM, p.n_rows, &grid);
+    cudaError_t e = norm_grid(norm_bwd_kernel<T, VEC, TEAM, NV>, threads, threads / TEAM, smem, p.n_rows, &grid);
     if (e != cudaSuccess)
         return e;
     *blocks = grid;
-    return plan ? cudaSuccess : launch_pdl(norm_bwd_kernel<T, VEC, TEAM, NV>, dim3(grid), dim3(threads), st, p, partial);
+    return plan ? cudaSuccess : launch_pdl(norm_bwd_kernel<T, VEC, TEAM, NV>, dim3(grid), dim3(threads), smem, st, p, partial);
 }
 
 template <typename T>
@@ -581,7 +711,7 @@ cudaError_t launch_norm_bwd(const NormBwdParams &p, float *partial, cudaStream_t
     cudaError_t e = norm_bwd_call(p, partial, &blocks, false, st);
     if (e != cudaSuccess || !p.grad_weight)
         return e;
-    return launch_pdl(norm_dweight_kernel, dim3((p.dim + 31) / 32), dim3(32, 32), st, partial, blocks, p.dim, p.grad_weight);
+    return launch_pdl(norm_dweight_kernel, dim3((p.dim + 31) / 32), dim3(32, 32), 0, st, partial, blocks, p.dim, p.grad_weight);
 }
 
 }  // namespace csa

@@ -89,10 +89,13 @@ int csa_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, int6
         CSA_TRY(check_ptr(scales, "scales", 4));
     csa::NormFwdParams p{x,     residual,   x_stride,  residual_stride, weight, n_rows, dim, eps, dtype,
                          slots, slots ? n_slots : n_rows, out, out_stride, out_dtype, scales, scale_group,
-                         residual_out, rstd};
+                         residual_out, rstd, nullptr, 0};
     if (out_dtype == CSA_DTYPE_E4M3 && scale_group == 128 && !csa::norm_fwd_vectors(p))
         return fail_status(CSA_ERR_MISALIGNED, "scale_group 128 needs rows on 16-byte boundaries");
-    cudaError_t e = csa::launch_norm_fwd(p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = csa::device_facts(nullptr, nullptr, &p.status);
+    if (e != cudaSuccess)
+        return cuda_status(e, "device set-up");
+    e = csa::launch_norm_fwd(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CSA_OK : cuda_status(e, "norm launch");
 }
 
@@ -121,10 +124,10 @@ int csa_rms_norm_bwd(const void *h, int64_t h_stride, const void *grad_out, int6
     CSA_TRY(check_ptr(rstd, "rstd", 4));
     CSA_TRY(check_ptr(grad_x, "grad_x", eb));
     csa::NormBwdParams p{h,      grad_out, grad_residual, h_stride, grad_out_stride, grad_residual_stride, weight, rstd,
-                         n_rows, dim,      dtype,         grad_x,   grad_weight};
+                         n_rows, dim,      dtype,         grad_x,   grad_weight, nullptr, 0};
     int blocks = 0;
     cudaMemPool_t pool = nullptr;
-    cudaError_t e = csa::device_facts(nullptr, &pool, nullptr);
+    cudaError_t e = csa::device_facts(nullptr, &pool, &p.status);
     if (e == cudaSuccess)
         e = csa::norm_bwd_blocks(p, &blocks);
     if (e != cudaSuccess)

@@ -25,6 +25,8 @@ struct NormFwdParams {
     int scale_group;
     void *residual_out;
     float *rstd;
+    unsigned *status;
+    int stages;  // (set by the launcher) rows in a block's ring
 };
 bool norm_fwd_vectors(const NormFwdParams &p);
 cudaError_t launch_norm_fwd(const NormFwdParams &p, cudaStream_t st);
@@ -37,6 +39,8 @@ struct NormBwdParams {
     int dim, dtype;
     void *grad_x;
     float *grad_weight;
+    unsigned *status;
+    int stages;  // (set by the launcher) rows in a block's ring
 };
 // blocks of the launch on the current device = rows of [blocks, dim] partial sums that it writes
 cudaError_t norm_bwd_blocks(const NormBwdParams &p, int *blocks);
