@@ -90,7 +90,7 @@ int csa_rms_norm_fwd(const void *x, int64_t x_stride, const void *residual, int6
     csa::NormFwdParams p{x,     residual,   x_stride,  residual_stride, weight, n_rows, dim, eps, dtype,
                          slots, slots ? n_slots : n_rows, out, out_stride, out_dtype, scales, scale_group,
                          residual_out, rstd, nullptr, 0};
-    if (out_dtype == CSA_DTYPE_E4M3 && scale_group == 128 && !csa::norm_fwd_vectors(p))
+    if (out_dtype == CSA_DTYPE_E4M3 && scale_group == 128 && !csa::norm_fwd_whole_vectors(p))
         return fail_status(CSA_ERR_MISALIGNED, "scale_group 128 needs rows on 16-byte boundaries");
     cudaError_t e = csa::device_facts(nullptr, nullptr, &p.status);
     if (e != cudaSuccess)

@@ -28,7 +28,7 @@ struct NormFwdParams {
     unsigned *status;
     int stages;  // (set by the launcher) rows in a block's ring
 };
-bool norm_fwd_vectors(const NormFwdParams &p);
+bool norm_fwd_whole_vectors(const NormFwdParams &p);
 cudaError_t launch_norm_fwd(const NormFwdParams &p, cudaStream_t st);
 
 struct NormBwdParams {
