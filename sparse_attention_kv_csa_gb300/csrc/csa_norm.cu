@@ -32,6 +32,8 @@ norm_fwd_kernel(const NormFwdParams p)
             const int c = (i * TEAM + t) * VEC + k;
             w[i][k] = c < p.dim ? (p.weight ? __ldg(p.weight + c) : 1.0f) : 0.0f;
         }
+    // 128 columns lie in 128 / VEC neighbouring lanes; the host takes that form with whole vectors only
+    const bool grouped = VEC * sizeof(T) == 16 && p.scale_group == 128;
     const float inv_dim = 1.0f / (float)p.dim;
     const int64_t step = (int64_t)gridDim.x * kTeams;
     const int64_t passes = (p.n_rows + step - 1) / step;
@@ -63,7 +65,7 @@ norm_fwd_kernel(const NormFwdParams p)
     for (int64_t it = 0; it < passes; ++it, row += step) {
         const bool live = row < p.n_rows;
         float h[NV][VEC];
-        float ss = 0.0f;
+        float2 ss2 = splat(0.0f);
         if (STAGED && live) {
             // (a wait that gives up sets the device's status word; the rows' results are then wrong, as documented)
             mbar_wait(smem_addr(full + stage), phase, ring.status);
@@ -93,9 +95,7 @@ norm_fwd_kernel(const NormFwdParams p)
                         store<T, VEC>(static_cast<T *>(p.residual_out) + row * p.dim + c, hp);
                     unpack(hp, h[i]);
                 }
-#pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    ss = fmaf(h[i][k], h[i][k], ss);
+                ss2 = dot_add(h[i], h[i], ss2);
             } else {
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
@@ -103,7 +103,7 @@ norm_fwd_kernel(const NormFwdParams p)
             }
         }
         fetch(row + step);
-        ss = team_reduce<TEAM, false>(ss, buf[it & 1]);
+        const float ss = team_reduce<TEAM, false>(ss2.x + ss2.y, buf[it & 1]);
         if (STAGED) {
             // the sum's barrier: the whole team has read the stage
             if (TEAM == 32)
@@ -125,14 +125,29 @@ norm_fwd_kernel(const NormFwdParams p)
         }
         const bool write = live && to >= 0 && to < p.n_slots;
         float amax = 0.0f;
+        // (a NaN among the y needs a sum that is not finite; the plain maximum drops NaN)
+        const bool odd = !(ss < INFINITY);
+        auto magnitude = [&](int i, float m) {
+            if (odd) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+                for (int k = 0; k < VEC; ++k)
+                    m = max_nan(m, fabsf(h[i][k]));
+            } else {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                h[i][k] = h[i][k] * rstd * w[i][k];
-                if (kBits8)
-                    amax = max_nan(amax, fabsf(h[i][k]));
+                for (int k = 0; k < VEC; ++k)
+                    m = fmaxf(m, fabsf(h[i][k]));
             }
+            return m;
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            scale_by(h[i], rstd);
+            scale_by(h[i], w[i]);
+            if (kBits8 && !grouped)
+                amax = magnitude(i, amax);
+        }
+        if (kBits8 && !grouped)
+            amax = team_reduce<TEAM, true>(amax, buf[2 + (it & 1)]);
         OUT *out = static_cast<OUT *>(p.out) + to * p.out_stride;
         if constexpr (!kBits8) {
             if (write)
@@ -143,18 +158,11 @@ norm_fwd_kernel(const NormFwdParams p)
                         store<OUT, VEC>(out + c, pack<OUT, VEC>(h[i]));
                 }
         } else {
-            // 128 columns lie in 128 / VEC neighbouring lanes; the host takes that form with whole vectors only
-            const bool grouped = VEC * sizeof(T) == 16 && p.scale_group == 128;
-            if (!grouped)
-                amax = team_reduce<TEAM, true>(amax, buf[2 + (it & 1)]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TEAM + t) * VEC;
                 if (grouped) {
-                    amax = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        amax = max_nan(amax, fabsf(h[i][k]));
+                    amax = magnitude(i, 0.0f);
 #pragma unroll
                     for (int o = 64 / VEC; o; o >>= 1)
                         amax = max_nan(amax, __shfl_xor_sync(~0u, amax, o));
@@ -170,15 +178,16 @@ norm_fwd_kernel(const NormFwdParams p)
 #pragma unroll
                         for (int k = 0; k < VEC; ++k)
                             h[i][k] /= scale;
+                    scale_by(h[i], inv);
                     if constexpr (VEC > 1) {
 #pragma unroll
                         for (int k = 0; k < VEC; k += 2) {
                             const __nv_fp8x2_storage_t two =
-                                __nv_cvt_float2_to_fp8x2(make_float2(h[i][k] * inv, h[i][k + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                                __nv_cvt_float2_to_fp8x2(make_float2(h[i][k], h[i][k + 1]), __NV_SATFINITE, __NV_E4M3);
                             memcpy(&o.v[k], &two, 2);
                         }
                     } else {
-                        o.v[0] = __nv_cvt_float_to_fp8(h[i][0] * inv, __NV_SATFINITE, __NV_E4M3);
+                        o.v[0] = __nv_cvt_float_to_fp8(h[i][0], __NV_SATFINITE, __NV_E4M3);
                     }
                     store<__nv_fp8_storage_t, VEC>(reinterpret_cast<__nv_fp8_storage_t *>(out) + c, o);
                     if (grouped ? (c & 127) == 0 : c == 0)

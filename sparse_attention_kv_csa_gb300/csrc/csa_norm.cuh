@@ -126,7 +126,50 @@ template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> pack(cons
     return a;
 }
 
-// Sum (or NaN-propagating maximum of magnitudes) over a team of TEAM threads, the same value and order in every
+// Elementwise work in fp32 pairs where there are any: these kernels are bound by instructions as much as by bytes on
+// narrow rows (131288 rows of 512 with 8-bit output: 470 instructions a row of a warp without the pairs, 72 us).
+template <int VEC> __device__ __forceinline__ void scale_by(float (&v)[VEC], float a)
+{
+    if constexpr (VEC > 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            const float2 r = mul2(make_float2(v[k], v[k + 1]), splat(a));
+            v[k] = r.x;
+            v[k + 1] = r.y;
+        }
+    } else {
+        v[0] *= a;
+    }
+}
+
+template <int VEC> __device__ __forceinline__ void scale_by(float (&v)[VEC], const float (&a)[VEC])
+{
+    if constexpr (VEC > 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            const float2 r = mul2(make_float2(v[k], v[k + 1]), make_float2(a[k], a[k + 1]));
+            v[k] = r.x;
+            v[k + 1] = r.y;
+        }
+    } else {
+        v[0] *= a[0];
+    }
+}
+
+// c + a b, by pairs: c.x takes the even elements, c.y the odd ones.
+template <int VEC> __device__ __forceinline__ float2 dot_add(const float (&a)[VEC], const float (&b)[VEC], float2 c)
+{
+    if constexpr (VEC > 1) {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2)
+            c = fma2(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]), c);
+    } else {
+        c.x = fmaf(a[0], b[0], c.x);
+    }
+    return c;
+}
+
+// Sum (or maximum, NaN if there is one) over a team of TEAM threads, the same value and order in every
 // thread.  buf: one float per warp of the block, not in use by an earlier unfinished call.
 template <int TEAM, bool MAX> __device__ __forceinline__ float team_reduce(float v, float *buf)
 {
@@ -200,8 +243,8 @@ cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_
 
 // Rows in a team's ring: the block's rings 24 KB in the forward (64 KB leave too few blocks an SM: 93 against 79 us for
 // 16411 rows of 4096 with 8-bit output) and 40 KB in the backward (28 to 64 KB measured alike), one row where two would
-// not fit.  No ring where every team has one row at most: loads into registers then start sooner (6.5 against 7.6 us for
-// 8256 rows of 512).
+// not fit.  No ring where a team has three rows at most: loads into registers then start sooner (6.5 against 7.6 us for
+// 8256 rows of 512 with 8-bit output, some 2.3 rows a team).
 constexpr int kRingForward = 24 * 1024, kRingBackward = 40 * 1024;
 
 int ring_stages(int row_bytes, int arrays, int teams, int block_bytes)
@@ -222,7 +265,7 @@ cudaError_t norm_plan(Kernel plain, Kernel staged, int threads, int teams, int r
     *stages = 0;
     *smem = 0;
     cudaError_t e = resident_blocks(reinterpret_cast<const void *>(plain), threads, 0, 1, &resident);
-    if (e == cudaSuccess && plain != staged && want > resident) {
+    if (e == cudaSuccess && plain != staged && want > 3 * (int64_t)resident) {
         *k = staged;
         *stages = ring_stages(row_bytes, arrays, teams, block_bytes);
         *smem = (size_t)*stages * row_bytes * arrays * teams;

@@ -66,11 +66,11 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
     auto values = [&](const Row &x, int i, float (&unit)[VEC], float (&g)[VEC], float (&raw)[VEC]) {
         unpack(x.h[i], unit);
         unpack(x.g[i], raw);
+        scale_by(unit, x.rstd);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            unit[k] *= x.rstd;
-            g[k] = raw[k] * (kRoomy ? w[i][k] : weight_at(i, k));
-        }
+        for (int k = 0; k < VEC; ++k)
+            g[k] = kRoomy ? w[i][k] : weight_at(i, k);
+        scale_by(g, raw);
     };
     Row now, next;
     auto refill = [&](int64_t r, int stage) {

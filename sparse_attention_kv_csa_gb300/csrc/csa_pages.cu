@@ -45,49 +45,50 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams 
     if (tid == 0)
         widest = 0;
     __syncthreads();
-    // exclusive prefix sums, 512 requests at a time; all sums are of whole numbers, so any order gives the same
-    int base_rows = 0, base_pages = 0, wide = 0;
-    for (int at = 0; at < n; at += kThreads) {
-        const int r = at + tid;
-        int rows = 0, pages = 0;
-        if (r < n) {
-            const Req q = request(p, r);
-            rows = q.new_rows - q.old_rows;
-            pages = q.need - q.held;
-            wide = max(wide, q.need);
-        }
-        int a = rows, b = pages;
+    // Exclusive prefix sums: a thread adds up a stretch of requests, the threads' sums are scanned, the thread goes over
+    // its stretch again.  All sums are of whole numbers, so any order gives the same.
+    const int per = (n + kThreads - 1) / kThreads, lo = min(n, tid * per), hi = min(n, lo + per);
+    int rows = 0, pages = 0, wide = 0;
+#pragma unroll 4
+    for (int r = lo; r < hi; ++r) {
+        const Req q = request(p, r);
+        rows += q.new_rows - q.old_rows;
+        pages += q.need - q.held;
+        wide = max(wide, q.need);
+    }
+    int a = rows, b = pages;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int ua = __shfl_up_sync(~0u, a, o), ub = __shfl_up_sync(~0u, b, o);
-            if (lane >= o) {
-                a += ua;
-                b += ub;
-            }
+    for (int o = 1; o < 32; o <<= 1) {
+        const int ua = __shfl_up_sync(~0u, a, o), ub = __shfl_up_sync(~0u, b, o);
+        if (lane >= o) {
+            a += ua;
+            b += ub;
         }
-        if (lane == 31) {
-            part[0][warp] = a;
-            part[1][warp] = b;
-        }
-        __syncthreads();
-        int wa = base_rows, wb = base_pages, ta = 0, tb = 0;
+    }
+    if (lane == 31) {
+        part[0][warp] = a;
+        part[1][warp] = b;
+    }
+    __syncthreads();
+    int base_rows = 0, base_pages = 0;
+    a -= rows;
+    b -= pages;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
-            const int pa = part[0][i], pb = part[1][i];
-            if (i < warp) {
-                wa += pa;
-                wb += pb;
-            }
-            ta += pa;
-            tb += pb;
+    for (int i = 0; i < kThreads / 32; ++i) {
+        const int pa = part[0][i], pb = part[1][i];
+        if (i < warp) {
+            a += pa;
+            b += pb;
         }
-        if (r < n) {
-            cu_rows[r] = wa + a - rows;
-            cu_pages[r] = wb + b - pages;
-        }
-        base_rows += ta;
-        base_pages += tb;
-        __syncthreads();
+        base_rows += pa;
+        base_pages += pb;
+    }
+    for (int r = lo; r < hi; ++r) {
+        const Req q = request(p, r);
+        cu_rows[r] = a;
+        cu_pages[r] = b;
+        a += q.new_rows - q.old_rows;
+        b += q.need - q.held;
     }
     if (tid == 0) {
         cu_rows[n] = base_rows;
@@ -122,13 +123,23 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams 
         const int64_t add = (int64_t)cu_pages[r] - q.held;
         const int64_t in_row = (int64_t)r * p.table_stride, out_row = (int64_t)r * p.width;
         const int end = min(p.width, c0 + 512);
-        for (int c = c0 + lane; c < end; c += 32) {
-            int id = -1;
-            if (c < q.held)
-                id = p.table[in_row + c];
-            else if (c < q.need)
-                id = fresh(add + c);
-            p.table_out[out_row + c] = id;
+        for (int c = c0 + lane; c < end; c += 32 * 4) {
+            int id[4];  // four loads under way
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int cu = c + 32 * u;
+                id[u] = -1;
+                if (cu < end) {
+                    if (cu < q.held)
+                        id[u] = p.table[in_row + cu];
+                    else if (cu < q.need)
+                        id[u] = fresh(add + cu);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (c + 32 * u < end)
+                    p.table_out[out_row + c + 32 * u] = id[u];
         }
     }
     // slots: the request of row i by bisection of the offsets in shared memory
