@@ -271,61 +271,64 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             items[p.n_req] = run;
         __syncthreads();
         const int per = (run + kThreads - 1) / kThreads, lo = min(run, tid * per), hi = min(run, lo + per);
-        auto walk = [&](auto &&visit) {
-            if (lo >= hi)
-                return;
-            int r = 0;  // items[r] <= lo < items[r + 1]
-            for (int top = p.n_req; top - r > 1;) {
-                const int mid = (r + top) >> 1;
-                if (items[mid] <= lo)
-                    r = mid;
-                else
-                    top = mid;
-            }
-            Request q = fact(r);
-            int m = lo - items[r];
-            for (int i = lo; i < hi; ++i, ++m) {
-                while (m >= q.items) {
-                    q = fact(++r);
-                    m = 0;
+        // Two passes of one loop (its instructions are fetched once): a thread's units, then, with the sums before it
+        // known, which item the block's first unit lies in.
+        long long mine = 0, first = 0, total = 0, from = 0;
+        bool here = true;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            if (lo < hi && here) {
+                int r = 0;  // items[r] <= lo < items[r + 1]
+                for (int top = p.n_req; top - r > 1;) {
+                    const int mid = (r + top) >> 1;
+                    if (items[mid] <= lo)
+                        r = mid;
+                    else
+                        top = mid;
                 }
-                visit(r, m, q, item_tiles<R>(p, q, m) + 1);
+                Request q = fact(r);
+                int m = lo - items[r];
+                long long at = first;
+                for (int i = lo; i < hi; ++i, ++m) {
+                    while (m >= q.items) {
+                        q = fact(++r);
+                        m = 0;
+                    }
+                    const int units = item_tiles<R>(p, q, m) + 1;
+                    if (pass == 1 && from >= at && from < at + units) {
+                        s.r = r;
+                        s.m = m;
+                        s.off = (int)(from - at);
+                        s.first[0] = q.first;
+                        s.first[1] = q.nq;
+                        s.first[2] = q.before;
+                        s.first[3] = q.items;
+                    }
+                    at += units;
+                }
+                mine = at - first;
             }
-        };
-        long long mine = 0;
-        walk([&](int, int, const Request &, int units) { mine += units; });
-        long long a = mine;
+            if (pass == 0) {
+                long long a = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(~0u, a, o);
-            if (lane >= o)
-                a += u;
-        }
-        if (lane == 31)
-            s.sums[warp] = a;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            before += i < warp ? s.sums[i] : 0;
-            total += s.sums[i];
-        }
-        const long long first = before + a - mine;
-        const int g = sharing(total, plan.blocks);
-        const long long from = cut(total, blockIdx.x, g);
-        if (blockIdx.x < g && from >= first && from < first + mine) {
-            long long at = first;
-            walk([&](int r, int m, const Request &q, int units) {
-                if (from >= at && from < at + units) {
-                    s.r = r;
-                    s.m = m;
-                    s.off = (int)(from - at);
-                    s.first[0] = q.first;
-                    s.first[1] = q.nq;
-                    s.first[2] = q.before;
-                    s.first[3] = q.items;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long u = __shfl_up_sync(~0u, a, o);
+                    if (lane >= o)
+                        a += u;
                 }
-                at += units;
-            });
+                if (lane == 31)
+                    s.sums[warp] = a;
+                __syncthreads();
+                long long before = 0;
+                for (int i = 0; i < kThreads / 32; ++i) {
+                    before += i < warp ? s.sums[i] : 0;
+                    total += s.sums[i];
+                }
+                first = before + a - mine;
+                const int g = sharing(total, plan.blocks);
+                from = cut(total, blockIdx.x, g);
+                here = blockIdx.x < g && from >= first && from < first + mine;
+            }
         }
         if (tid == 0)
             s.total = total;
@@ -918,46 +921,65 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
     }
 }
 
-// Joins the parts of the items that cross block boundaries: block (c, y) takes four rows of the item whose first part
-// block c of the kernel above wrote (its slot 1), with the slots 0 of the blocks after it up to the item's last.
-__global__ void __launch_bounds__(512) latent_join_kernel(const AttnParams p, const MmaPlan plan)
+// Joins the parts of the items that cross block boundaries: a warp a row, block (c, y) four rows of the item whose first
+// part block c of the kernel above wrote (its slot 1), with the slots 0 of the blocks after it up to the item's last.
+// Lane k finds the weight of part k, the parts are added in order.  Bound by the latency of three dependent reads.
+__global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, const MmaPlan plan)
 {
     pdl_wait();
     pdl_trigger();
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int4 j = plan.joins[c];
-    const int row = blockIdx.y * 4 + threadIdx.y;
+    const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
     if (!j.w || row >= j.y)
         return;
     const int64_t out_row = (int64_t)j.x + row;
-    const int head = (int)(out_row % p.n_heads);
-    const float sink = p.sink ? __ldg(p.sink + head) * kLog2E : -INFINITY;
-    auto part = [&](int k) { return (k == c ? 2 * (int64_t)c + 1 : 2 * (int64_t)k) * kTile + row; };
+    const int n = j.z - c + 1;
+    const float sink = p.sink ? __ldg(p.sink + out_row % p.n_heads) * kLog2E : -INFINITY;
+    auto part = [&](int k) { return (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * kTile + row; };
     float top = sink;
-    for (int k = c; k <= j.z; ++k)
+    for (int k = lane; k < n; k += 32)
         top = fmaxf(top, plan.part_ml[part(k)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
-    float tot = exp2_fast(sink - ref);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int col = threadIdx.x * 4;
-    for (int k = c; k <= j.z; ++k) {
-        const int64_t at = part(k);
-        const float2 ml = plan.part_ml[at];
-        const float w = exp2_fast(ml.x - ref);
-        tot = fmaf(w, ml.y, tot);
-        if (col < p.v_dim) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(plan.part_o + at * p.v_dim + col));
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
+    float tot = lane == 0 ? exp2_fast(sink - ref) : 0.0f;
+    float4 o[4] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        float w = 0.0f;
+        if (k0 + lane < n) {
+            const float2 ml = plan.part_ml[part(k0 + lane)];
+            w = exp2_fast(ml.x - ref);
+            tot = fmaf(w, ml.y, tot);
+        }
+        const int some = min(32, n - k0);
+#pragma unroll 2
+        for (int k = 0; k < some; ++k) {
+            const float wk = __shfl_sync(~0u, w, k);
+            const float *src = plan.part_o + part(k0 + k) * p.v_dim + lane * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lane * 4 + 128 * i < p.v_dim) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + 128 * i));
+                    o[i].x = fmaf(wk, v.x, o[i].x);
+                    o[i].y = fmaf(wk, v.y, o[i].y);
+                    o[i].z = fmaf(wk, v.z, o[i].z);
+                    o[i].w = fmaf(wk, v.w, o[i].w);
+                }
         }
     }
+#pragma unroll
+    for (int i = 16; i; i >>= 1)
+        tot += __shfl_xor_sync(~0u, tot, i);
     const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-    if (col < p.v_dim)
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + out_row * p.v_dim + col) =
-            make_uint2(f2_to_bf16x2(make_float2(o.x * inv, o.y * inv)), f2_to_bf16x2(make_float2(o.z * inv, o.w * inv)));
-    if (p.lse && threadIdx.x == 0)
+    uint16_t *dst = static_cast<uint16_t *>(p.out) + out_row * p.v_dim + lane * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (lane * 4 + 128 * i < p.v_dim)
+            *reinterpret_cast<uint2 *>(dst + 128 * i) = make_uint2(f2_to_bf16x2(make_float2(o[i].x * inv, o[i].y * inv)),
+                                                                  f2_to_bf16x2(make_float2(o[i].z * inv, o[i].w * inv)));
+    if (p.lse && lane == 0)
         p.lse[out_row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
 }
 
@@ -987,7 +1009,7 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     if (e != cudaSuccess)
         return e;
     cfg.gridDim = dim3(plan.blocks, kTile / 4);
-    cfg.blockDim = dim3((p.v_dim + 3) / 4, 4);
+    cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, plan);
 }
