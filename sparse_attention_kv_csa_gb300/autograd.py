@@ -1,4 +1,4 @@
-"""Training-side wrapper: the Compressor as a ``torch.autograd.Function``.
+"""Training-side wrappers: the Compressor and the root-mean-square norm as ``torch.autograd.Function``s.
 
 ``compress(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, capacity)``
 returns ``out`` ([capacity, head_dim] bf16) and, when autograd asks for it,
@@ -17,9 +17,9 @@ be modified in place between the two passes (autograd's version counter checks).
 """
 import torch
 
-from . import csa_compress_bwd, csa_compress_fwd
+from . import csa_compress_bwd, csa_compress_fwd, rms_norm_backward, rms_norm_forward
 
-__all__ = ["CompressFunction", "compress"]
+__all__ = ["CompressFunction", "compress", "RMSNormFunction", "rms_norm"]
 
 
 def _check_inputs(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, require_cuda=True):
@@ -79,3 +79,36 @@ class CompressFunction(torch.autograd.Function):
 def compress(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, capacity):
     """The Compressor's forward as a differentiable op (see the module docstring)."""
     return CompressFunction.apply(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, capacity)
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(out, h) = norm of h = x + residual; backward through csa_rms_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        out, _, total, rstd = rms_norm_forward(x, weight, eps, residual=residual)
+        ctx.save_for_backward(x if total is None else total, weight, rstd)
+        ctx.set_materialize_grads(False)
+        ctx.has_residual = residual is not None
+        return out, total
+
+    @staticmethod
+    def backward(ctx, grad_out, grad_total):
+        h, weight, rstd = ctx.saved_tensors
+        if grad_out is None:  # only the sum was used
+            return grad_total, None, grad_total if ctx.has_residual else None, None
+        grad_x, grad_weight = rms_norm_backward(grad_out.contiguous(), h, weight, rstd,
+                                                grad_residual=None if grad_total is None else grad_total.contiguous())
+        return grad_x, None if weight is None else grad_weight, grad_x if ctx.has_residual else None, None
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6):
+    """Differentiable root-mean-square norm over the last dimension of x (bf16, f16 or f32; weight fp32 or None).
+
+    Returns the norm of x, or with a residual (norm of x + residual, x + residual): the second is the residual stream,
+    through which gradients flow too.
+    """
+    shape = x.shape
+    flat = lambda t: None if t is None else t.reshape(-1, shape[-1])  # noqa: E731
+    out, total = RMSNormFunction.apply(flat(x), weight, flat(residual), eps)
+    return out.view(shape) if residual is None else (out.view(shape), total.view(shape))
