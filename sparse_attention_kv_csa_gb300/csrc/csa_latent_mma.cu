@@ -21,7 +21,7 @@
 //
 // Warps: 0-3 exponentials and output (each owns 16 query rows: its quarter of the lanes), 4 issues the MMAs.  Pages of
 // whole groups of bf16 rows: warp 5 issues TMA copies, warps 6-9 bring the next item's queries through registers.
-// Other pages, and 8-bit rows: warps 5-12 take turns at the groups, bring them to registers, widen 8-bit values to
+// Other pages, and 8-bit rows: warps 5 and on take turns at the groups, bring them to registers, widen 8-bit values to
 // bf16 (exact) and write the swizzled layout.  An 8-bit row's scale multiplies S by column and P before its rounding,
 // so it costs no precision.
 //
@@ -45,15 +45,21 @@ constexpr int kQueryChunk = kTile * 128;          // bytes of 64 columns of an i
 constexpr int kGroupChunk = 8 * 128;              // bytes of 64 columns of eight rows
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
-constexpr int kLoadWarps = 8;                     // rows through registers
+// Blocks an SM: two where the shared memory and tensor memory of each allow it (rows of up to 256 columns), whose waits
+// then overlap: 1024 tokens over 4096 rows of 128 columns 151 us with one, 109 with two, a decode step of 64 requests 31.6
+// and 27.5.  Rows through registers are brought by eight warps or, to leave registers for two blocks, four; for their
+// 256 columns one block is better (8-bit decode step 39.5 us, with two 40.9).
+constexpr int per_sm(Rows how, int nk) { return nk <= (how == kTma ? 4 : 3) ? 2 : 1; }
+constexpr int load_warps(Rows how, int nk) { return 8 / per_sm(how, nk); }
 constexpr int kTmaWarp = 5;                       // rows by TMA
 constexpr int kQueryWarps = 4;                    // rows by TMA: warps that bring queries
-template <Rows ROWS> constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + kLoadWarps);
+template <Rows ROWS, int NK>
+constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + load_warps(ROWS, NK));
 constexpr int kMaxStages = 4;
 // Units of a block's share at least.  Eight requests of 1024 rows: 26.1, 23.5 and 22.2 us with 4, 3 and 2; one of 16384
 // rows: 26.9, 27.6 and 32.0.
 constexpr int kMinUnits = 3;
-constexpr int kKept = 4096;                       // requests whose facts are kept in shared memory while work is cut
+constexpr int kKept = 2048;                       // requests whose facts are kept in shared memory while work is cut
 constexpr int kScores = 4;                        // S tiles in tensor memory
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -204,11 +210,12 @@ __device__ __forceinline__ int sharing(long long total, int blocks)
 }
 
 template <Rows ROWS, int NK, int R>
-__global__ void __launch_bounds__(kThreadsOf<ROWS>, 1)
+__global__ void __launch_bounds__(kThreadsOf<ROWS, NK>, per_sm(ROWS, NK))
 latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant__ CUtensorMap boxes,
                   const __grid_constant__ CUtensorMap groups, unsigned *status)
 {
-    constexpr int kThreads = kThreadsOf<ROWS>;
+    constexpr int kThreads = kThreadsOf<ROWS, NK>;
+    constexpr int kLoadWarps = load_warps(ROWS, NK);
     constexpr int kQueryArrivals = ROWS == kTma ? kQueryWarps : kLoadWarps;
     constexpr int kGroups = R / 8;
     constexpr int kGroupBytes = NK * kGroupChunk, kTileBytes = kGroups * kGroupBytes;
@@ -1036,7 +1043,7 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     cfg.numAttrs = 1;
     cfg.stream = st;
     cfg.gridDim = dim3(plan.blocks);
-    cfg.blockDim = dim3(kThreadsOf<ROWS>);
+    cfg.blockDim = dim3(kThreadsOf<ROWS, NK>);
     cfg.dynamicSmemBytes = plan.smem;
     e = cudaLaunchKernelEx(&cfg, kern, p, plan, boxes, groups, status);
     if (e != cudaSuccess)
@@ -1047,44 +1054,56 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, plan);
 }
 
-constexpr size_t kSmemLimit = 227 * 1024 - sizeof(Shared);
+// Dynamic shared memory of a block: what an SM has for one, or half of it, less the block's own.
+constexpr size_t smem_limit(Rows how, int nk) { return (per_sm(how, nk) == 2 ? 113 : 227) * 1024 - sizeof(Shared); }
 
 constexpr size_t fixed_of(int nk) { return (size_t)(nk + 1) * kQueryChunk + 1024; }  // queries, P, alignment
 
-constexpr int stages_of(int nk, int rows) { return (int)((kSmemLimit - fixed_of(nk)) / ((size_t)nk * rows * 128)); }
+constexpr int stages_of(Rows how, int nk, int rows)
+{
+    return (int)((smem_limit(how, nk) - fixed_of(nk)) / ((size_t)nk * rows * 128));
+}
 
 // Rows of a tile: the tensor core wants wide tiles, the loads want three tiles in flight; so 64 where three fit beside
 // the queries, else 48 (512 columns: a decode step of 64 requests 94.6 us against 97.5 with two tiles of 64 rows), else
 // (576 columns) two of 64 (608 tokens over 2048 rows 260 us against 305 with four of 32, which cost the tensor core as
 // much as 40 would).
-constexpr int rows_of(int nk) { return stages_of(nk, 64) < 3 && stages_of(nk, 48) >= 3 ? 48 : 64; }
+constexpr int rows_of(Rows how, int nk) { return stages_of(how, nk, 64) < 3 && stages_of(how, nk, 48) >= 3 ? 48 : 64; }
+
+Rows rows_how(const AttnParams &p)
+{
+    return p.cache_dtype == CSA_DTYPE_E4M3 ? kBits8 : p.page_size % 8 == 0 ? kTma : kRegisters;
+}
 
 MmaPlan make_plan(const AttnParams &p, int num_sms)
 {
     MmaPlan m{};
-    const int nk = p.head_dim / 64, rows = rows_of(nk);
-    m.stages = stages_of(nk, rows) > kMaxStages ? kMaxStages : stages_of(nk, rows);
+    const Rows how = rows_how(p);
+    const int nk = p.head_dim / 64, rows = rows_of(how, nk), fit = stages_of(how, nk, rows);
+    m.stages = fit > kMaxStages ? kMaxStages : fit;
     m.smem = fixed_of(nk) + (size_t)m.stages * nk * rows * 128;
-    m.p_buffers = m.smem + kQueryChunk <= kSmemLimit ? 2 : 1;
+    m.p_buffers = m.smem + kQueryChunk <= smem_limit(how, nk) ? 2 : 1;
     m.smem += (m.p_buffers - 1) * kQueryChunk;
     // the larger copy: the most groups that divide both the tile and the page
     for (m.box_groups = rows / 8; m.box_groups > 1 && (p.page_size % (8 * m.box_groups) || (rows / 8) % m.box_groups); --m.box_groups) {}
-    // more than half an SM's shared memory: one block an SM (it owns the tensor memory), and room for what cuts the work
+    // room for what cuts the work; one block an SM (it owns the tensor memory): more than half of the shared memory
     constexpr size_t least = 1024 + (kMaxRequests + 4) * sizeof(int) + kKept * sizeof(Request);
-    static_assert(least > 114 * 1024 && least < kSmemLimit, "");
-    m.smem = m.smem < least ? least : m.smem;
+    static_assert(least < smem_limit(kTma, 1), "");
+    const size_t floor_bytes = per_sm(how, nk) == 2 ? least : 116 * 1024;
+    m.smem = m.smem < floor_bytes ? floor_bytes : m.smem;
     m.tmem_columns = p.v_dim > 256 ? 512 : 256;  // O below, the S tiles above
-    m.blocks = num_sms;
+    m.blocks = num_sms * per_sm(how, nk);
     m.helpers = 16 * ((p.n_tokens * p.n_heads) / kTile + p.n_req) < m.blocks;  // (at least a bound of the items)
     return m;
 }
 
 template <int NK> cudaError_t go_rows(const AttnParams &p, const MmaPlan &m, unsigned *status, cudaStream_t st)
 {
-    constexpr int R = rows_of(NK);
-    if (p.cache_dtype == CSA_DTYPE_E4M3)
-        return go<kBits8, NK, R>(p, m, status, st);
-    return p.page_size % 8 == 0 ? go<kTma, NK, R>(p, m, status, st) : go<kRegisters, NK, R>(p, m, status, st);
+    switch (rows_how(p)) {
+    case kTma: return go<kTma, NK, rows_of(kTma, NK)>(p, m, status, st);
+    case kRegisters: return go<kRegisters, NK, rows_of(kRegisters, NK)>(p, m, status, st);
+    default: return go<kBits8, NK, rows_of(kBits8, NK)>(p, m, status, st);
+    }
 }
 
 }  // namespace
