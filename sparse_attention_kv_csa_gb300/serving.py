@@ -1,7 +1,8 @@
 """Serving the Compressor's rows: norm into a paged cache, page tables, attention over the cache.
 
 Argument checks and marshalling for the entry points of include/csa_serving.h; the arithmetic runs in the CUDA kernels
-of libcsa.so.  The helpers allocate their outputs with torch and launch on ``stream`` (a torch.cuda.Stream, a raw
+of libcsa.so.  Ordinary calls (contiguous tensors, the current stream) go through csa_torch, which checks, allocates and
+calls in C++; everything else, and every refusal, through the checks here.  The helpers allocate their outputs with torch and launch on ``stream`` (a torch.cuda.Stream, a raw
 cudaStream_t integer, or None for torch's current stream); no call synchronises.  Tensors live on the current CUDA
 device; ValueError / TypeError name an argument that does not fit, CSAError a call that the library refuses.
 
@@ -13,6 +14,9 @@ device; ValueError / TypeError name an argument that does not fit, CSAError a ca
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+
+from . import _build
 
 __all__ = ["csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention", "rms_norm_forward",
            "rms_norm_backward", "page_tables", "latent_attention"]
@@ -22,6 +26,8 @@ _raise = None
 _torch = None
 _Tensor = None
 _raw_stream = None
+_short = None  # csa_torch: the ordinary case of each helper in one call
+_e4m3 = None
 
 BF16, F16, F32, E4M3 = 0, 1, 2, 3
 _CODES = {}
@@ -43,8 +49,14 @@ def _bind(lib, check):
 
 def _load_torch():
     """torch is imported on first use, like in the rest of the package."""
-    global _torch, _Tensor, _raw_stream
+    global _torch, _Tensor, _raw_stream, _short, _e4m3
     import torch
+    spec = importlib.util.spec_from_file_location("csa_torch", _build.build_binding())
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
+                  ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention")))
+    _short, _e4m3 = module, torch.float8_e4m3fn
     _torch, _Tensor = torch, torch.Tensor
     # the current stream's handle without building a Stream object (some 3 us of a call of 10)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -176,8 +188,6 @@ def _pointer(t):
 
 def _matrix(name, t):
     """t's shape, code and device: a matrix in bf16, f16 or f32 on the current device."""
-    if _torch is None:
-        _load_torch()
     if not isinstance(t, _torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     code = _CODES.get(t.dtype, E4M3)
@@ -196,6 +206,13 @@ def rms_norm_forward(x, weight=None, eps=1e-6, residual=None, out_dtype=None, sc
     (int64 [n_rows], needs ``out`` and for 8 bits ``scales``): row i goes to out[slots[i]], nowhere when negative.
     Returns (out, scales or None, x + residual or None, rstd fp32 [n_rows]).
     """
+    if _torch is None:
+        _load_torch()
+    if stream is None and (out_dtype is None or out_dtype is _e4m3):
+        bits8 = out_dtype is _e4m3 or (out is not None and getattr(out, "dtype", None) is _e4m3)
+        r = _short.rms_norm_forward(x, weight, eps, residual, bits8, scale_group, slots, out, scales)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
     shape, code, d = _matrix("x", x)
     n, dim = shape
     dtype, device, f32 = x.dtype, x.device, _torch.float32
@@ -244,6 +261,12 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, stream=None
     h is the forward's x + residual (x without a residual), rstd its fourth result; grad_residual the gradient that
     reaches x + residual directly.
     """
+    if _torch is None:
+        _load_torch()
+    if stream is None:
+        r = _short.rms_norm_backward(grad_out, h, weight, rstd, grad_residual)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
     shape, code, d = _matrix("h", h)
     n, dim = shape
     dtype, device, f32 = h.dtype, h.device, _torch.float32
@@ -273,6 +296,10 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
     """
     if _torch is None:
         _load_torch()
+    if stream is None:
+        r = _short.page_tables(before, after, ratio, page_size, free_pages, block_table, capacity, taken, out)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
     i32 = _torch.int32
     if not isinstance(before, _torch.Tensor):
         raise TypeError("before must be a tensor")
@@ -311,6 +338,10 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
     """
     if _torch is None:
         _load_torch()
+    if stream is None:
+        r = _short.latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim, row_scales, sink, out)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
     bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
     if type(q) is not _Tensor or q.dtype is not bf16 or q.dim() != 3:
         _fits("q", q, bf16, (None, None, None), None)
