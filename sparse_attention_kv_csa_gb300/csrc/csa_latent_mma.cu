@@ -112,13 +112,14 @@ __device__ __forceinline__ Request request(const AttnParams &p, int r)
 __device__ __forceinline__ int visible(const AttnParams &p, const Request &q, int token)
 {
     const int held = q.before + token + 1;
-    return held <= 0 ? 0 : min(held / p.ratio, p.width * p.page_size);
+    return held <= 0 ? 0 : min((int)p.by_ratio.quotient((uint32_t)held), p.width * p.page_size);
 }
 
-// (all in 32 bits: a 64-bit division takes some 500 cycles, and the tokens times the heads stay below 2^31)
+// (all in 32 bits and by multiplication: the tokens times the heads stay below 2^31, and divisions, 64-bit ones above
+// all, made half of a block's first 7000 cycles)
 __device__ __forceinline__ int last_token(const AttnParams &p, const Request &q, int m)
 {
-    return (int)((min((uint32_t)(m + 1) * kTile, (uint32_t)q.nq * (uint32_t)p.n_heads) - 1) / (uint32_t)p.n_heads);
+    return (int)p.by_heads.quotient(min((uint32_t)(m + 1) * kTile, (uint32_t)q.nq * (uint32_t)p.n_heads) - 1);
 }
 
 template <int R> __device__ __forceinline__ int item_tiles(const AttnParams &p, const Request &q, int m)
@@ -378,10 +379,10 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             const int item_rows = min(kTile, w.q.nq * p.n_heads - w.item() * kTile);
             const int64_t out_row = (int64_t)w.q.first * p.n_heads + (int64_t)w.item() * kTile;
             auto seen_by = [&](int row) {
-                return row < item_rows ? visible(p, w.q, (w.item() * kTile + row) / p.n_heads) : 0;
+                return row < item_rows ? visible(p, w.q, (int)p.by_heads.quotient(w.item() * kTile + row)) : 0;
             };
             const int seen0 = seen_by(r0), seen1 = seen_by(r0 + 8);
-            const int all_see = visible(p, w.q, (int)((uint32_t)w.item() * kTile / (uint32_t)p.n_heads));
+            const int all_see = visible(p, w.q, (int)p.by_heads.quotient((uint32_t)w.item() * kTile));
             const int end = visible(p, w.q, last_token(p, w.q, w.item()));
             const bool whole = item_rows == kTile;
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // l: this thread's columns only
@@ -587,7 +588,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             if (done) {
                 // the factor that turns O into the result
                 auto finish = [&](int row, bool live, float m, float l) {
-                    const float sink = live && p.sink ? __ldg(p.sink + (w.item() * kTile + row) % p.n_heads) * kLog2E : -INFINITY;
+                    const float sink = live && p.sink ? __ldg(p.sink + p.by_heads.remainder(w.item() * kTile + row)) * kLog2E : -INFINITY;
                     const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
                     const float down = exp2_fast(m - ref), tot = l * down + exp2_fast(sink - ref);
                     if (live && p.lse && (lane & 3) == 0)
@@ -763,8 +764,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     const int row = (i * kQueryArrivals + lw) * 4 + (lane >> 3), flat = w.item() * kTile + row;
                     const uint8_t *src = static_cast<const uint8_t *>(p.q) + (lane & 7) * 16;
                     if (row < item_rows)
-                        src += ((int64_t)(w.q.first + flat / p.n_heads) * p.q_token_stride +
-                                (int64_t)(flat % p.n_heads) * p.q_head_stride) * 2;
+                        src += ((int64_t)(w.q.first + p.by_heads.quotient(flat)) * p.q_token_stride +
+                                (int64_t)p.by_heads.remainder(flat) * p.q_head_stride) * 2;
 #pragma unroll
                     for (int ch = 0; ch < NK; ++ch)
                         v[i][ch] = row < item_rows ? load_now(src + ch * 128) : zero4();
@@ -799,7 +800,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 constexpr bool kAhead = ROWS == kBits8;
                 constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
                 auto row_of = [&](int i) { return w.t0 * R + i * 8 + (lane & 7); };
-                auto look_up = [&](int i) { return i < n_groups && row_of(i) < end ? load_now(table + row_of(i) / p.page_size) : 0; };
+                auto look_up = [&](int i) { return i < n_groups && row_of(i) < end ? load_now(table + p.by_page.quotient(row_of(i))) : 0; };
                 struct Fetched {
                     uint4 v[kParts][NK];
                     float scale;
@@ -807,7 +808,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 };
                 auto fetch = [&](int i, int page, Fetched &f8) {
                     const bool need = i < n_groups && row_of(i) < end, found = page >= 0 && page < p.n_pages;
-                    const int64_t slot = need && found ? (int64_t)page * p.page_size + row_of(i) % p.page_size : -1;
+                    const int64_t slot = need && found ? (int64_t)page * p.page_size + p.by_page.remainder(row_of(i)) : -1;
                     f8.missing = __ballot_sync(~0u, need && !found) & 0xffu;
 #pragma unroll
                     for (int h = 0; h < kParts; ++h) {
@@ -896,13 +897,13 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
             // lane % 8 finds the page of one of a tile's groups, a tile ahead
             auto needed = [&](int t) { return t < w.t1 && (lane & 7) < kGroups && t * R + (lane & 7) * 8 < end; };
-            auto look_up = [&](int t) { return needed(t) ? load_now(table + (t * R + (lane & 7) * 8) / p.page_size) : 0; };
+            auto look_up = [&](int t) { return needed(t) ? load_now(table + p.by_page.quotient(t * R + (lane & 7) * 8)) : 0; };
             int next = look_up(w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++tile) {
                 const int st = tile % stages;
                 const bool need = needed(t), found = next >= 0 && next < p.n_pages;
                 const uint32_t missing = __ballot_sync(~0u, need && !found) & 0xffu;
-                const int at = need && found ? (next * p.page_size + (t * R + (lane & 7) * 8) % p.page_size) >> 3 : none;
+                const int at = need && found ? (next * p.page_size + (int)p.by_page.remainder(t * R + (lane & 7) * 8)) >> 3 : none;
                 next = look_up(t + 1);
                 if (tile >= stages) {
                     ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
@@ -956,7 +957,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, co
     if (row >= j.y || mine >= (shared ? units : 1))
         return;
     const int64_t out_row = (int64_t)j.x + row;
-    const float sink = p.sink ? __ldg(p.sink + out_row % p.n_heads) * kLog2E : -INFINITY;
+    const float sink = p.sink ? __ldg(p.sink + p.by_heads.remainder((uint32_t)out_row)) * kLog2E : -INFINITY;
     auto part = [&](int k) { return (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * kTile + row; };
     float top = sink;
     for (int k = lane; k < n; k += 32)

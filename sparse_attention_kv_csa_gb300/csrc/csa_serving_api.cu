@@ -229,7 +229,8 @@ int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     csa::AttnParams p{q,       q_token_stride, q_head_stride, cu_q,        n_req,        n_tokens, n_heads, head_dim, v_dim,
                       cache,   cache_stride,   cache_dtype,   cache_dtype == CSA_DTYPE_E4M3 ? row_scales : nullptr,
                       n_pages, page_size,      block_table,   table_stride, n_pages > 0 ? width : 0, seq_lens, ratio, scale, sink,
-                      out,     lse};
+                      out,     lse,
+                      csa::Divider((uint32_t)n_heads), csa::Divider((uint32_t)ratio), csa::Divider((uint32_t)page_size)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!csa::latent_mma_supported(p)) {
         cudaError_t e = csa::launch_attention_plain(p, st);
