@@ -25,7 +25,7 @@
 // bf16 (exact) and write the swizzled layout.  An 8-bit row's scale multiplies S by column and P before its rounding,
 // so it costs no precision.
 //
-// Work is cut evenly: item i counts one unit for its queries and output and one for each tile; block c takes the units
+// Work is cut evenly: an item counts three units for its queries and output and one for each tile; block c takes the units
 // [c T / G, (c+1) T / G) of the T units.  Items that cross a cut leave (O, m, l) of their parts in the workspace and a
 // second kernel joins them in order.  Nothing else depends on the grid, and no order on timing.
 #include <cuda.h>
@@ -56,6 +56,9 @@ constexpr int kQueryWarps = 4;                    // rows by TMA: warps that bri
 template <Rows ROWS, int NK>
 constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + load_warps(ROWS, NK));
 constexpr int kMaxStages = 4;
+// Units of an item besides its tiles, for its queries and output: a decode step of 64 requests 83.8, 81.2 and 80.2 us with
+// 1, 2 and 3, of 129 requests with 8-bit rows 150.2, 148.0 and 145.4.
+constexpr int kHead = 3;
 // Units of a block's share at least.  Eight requests of 1024 rows: 26.1, 23.5 and 22.2 us with 4, 3 and 2; one of 16384
 // rows: 26.9, 27.6 and 32.0.
 constexpr int kMinUnits = 3;
@@ -149,10 +152,10 @@ template <int R> struct Walk {
                 q = request(p, r);
             }
             nt = item_tiles<R>(p, q, m);
-            const int take = (int)min((long long)(nt + 1 - off), left);
+            const int take = (int)min((long long)(nt + kHead - off), left);
             const bool head = off == 0;
-            t0 = max(off - 1, 0);
-            t1 = off + take - 1;
+            t0 = max(off - kHead, 0);
+            t1 = max(off + take - kHead, 0);
             left -= take;
             off = 0;
             ++m;
@@ -311,7 +314,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         q = fact(++r);
                         m = 0;
                     }
-                    const int units = item_tiles<R>(p, q, m) + 1;
+                    const int units = item_tiles<R>(p, q, m) + kHead;
                     if (pass == 1 && from >= at && from < at + units) {
                         s.r = r;
                         s.m = m;
@@ -944,7 +947,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
 // units of 32, from unit i on in steps of n, and reads four parts of a unit at once, eight lanes each (one request of
 // 16384 rows, 85 parts: 41.8 us with part 0 alone, 27.4 so; 16 items of ten parts: 42.0 and 48.3).  Sums run over the
 // parts in a fixed order.  Bound by the latency of three dependent reads and by the launches of blocks that find no part.
-__global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, const MmaPlan plan)
+template <bool HELPERS> __global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, const MmaPlan plan)
 {
     pdl_wait();
     pdl_trigger();
@@ -953,7 +956,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, co
     const int lane = threadIdx.x & 31, row = blockIdx.y * 4 + (threadIdx.x >> 5);
     const int4 j = plan.joins[slot];
     const int c = j.z, n = j.w - c + 1, mine = slot / 2 - c, units = p.v_dim / 32;
-    const bool shared = plan.helpers && n > 4;
+    const bool shared = HELPERS && n > 4;
     if (row >= j.y || mine >= (shared ? units : 1))
         return;
     const int64_t out_row = (int64_t)j.x + row;
@@ -987,7 +990,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const AttnParams p, co
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + out_row * p.v_dim + col) =
             make_uint2(f2_to_bf16x2(make_float2(o.x * inv, o.y * inv)), f2_to_bf16x2(make_float2(o.z * inv, o.w * inv)));
     };
-    if (!shared) {
+    if (!HELPERS || !shared) {
         float4 o[4] = {};
 #pragma unroll 2
         for (int k = 0; k < n; ++k) {
@@ -1052,7 +1055,8 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     cfg.gridDim = dim3((plan.helpers ? 2 : 1) * plan.blocks, kTile / 4);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel, p, plan);
+    return plan.helpers ? cudaLaunchKernelEx(&cfg, latent_join_kernel<true>, p, plan)
+                        : cudaLaunchKernelEx(&cfg, latent_join_kernel<false>, p, plan);
 }
 
 // Dynamic shared memory of a block: what an SM has for one, or half of it, less the block's own.
