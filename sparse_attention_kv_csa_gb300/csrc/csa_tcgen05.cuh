@@ -6,6 +6,20 @@
 
 namespace csa {
 
+// Whether the barrier's phase is complete, without waiting (mbar_wait waits).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // ------------------------------------------------------- tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns)
