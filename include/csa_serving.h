@@ -8,7 +8,9 @@
  * launches nothing.  Kernels are programmatic dependents of their stream predecessor.  Workspace comes from the
  * library's stream-ordered pool, allocated and released in stream order inside the call, so calls can be captured
  * into CUDA graphs (make the first call on a device before the capture).  Results do not depend on what ran before
- * and are bitwise reproducible; no floating-point atomics.
+ * and are bitwise reproducible; no floating-point atomics.  Kernels bound their waits on shared-memory barriers as the
+ * Compressor's do: one that expires is recorded in the device's status word (csa_device_status), and that call's results
+ * are not valid.
  */
 #ifndef CSA_SERVING_H_
 #define CSA_SERVING_H_
@@ -37,7 +39,8 @@ typedef enum csa_dtype {
  * or NULL (ones).  out_dtype: dtype or E4M3.  slots: int64 [n_rows] or NULL; row i goes to row slots[i] of out and
  * scales, and nowhere when slots[i] is outside [0, n_slots) (distinct rows need distinct slots); without slots row i
  * goes to row i and n_slots is ignored.  scales: fp32 [rows of out, groups], E4M3 only.  residual_out (h, contiguous) and rstd (fp32
- * [n_rows]) may be NULL.  out and residual_out may be x or residual themselves (same stride), else must not overlap.
+ * [n_rows]) may be NULL.  Without slots out and residual_out may be x or residual themselves (same stride); otherwise
+ * outputs overlap no input.
  * dim in [1, 16384]; scale_group 128 needs dim a multiple of 128 and 16-byte aligned bases and strides
  * (CSA_ERR_MISALIGNED); everything else takes any alignment of its elements, faster where rows are 16-byte aligned.
  */
@@ -97,7 +100,8 @@ CSA_API int csa_page_tables(const int32_t *before, const int32_t *after, int32_t
  * sink       fp32 [n_heads] or NULL
  * out        bf16 [n_tokens, n_heads, v_dim] contiguous;  lse fp32 [n_tokens, n_heads] or NULL
  *
- * head_dim: a multiple of 8 in [8, 1024], v_dim a multiple of 8 in [8, head_dim].  Multiples of 64 up to head_dim 576
+ * n_req <= 14000, n_heads <= 4096, n_tokens * n_heads < 2^31; n_pages * page_size and width * page_size at most
+ * 2^31 - 128.  head_dim: a multiple of 8 in [8, 1024], v_dim a multiple of 8 in [8, head_dim].  Multiples of 64 up to head_dim 576
  * and v_dim 512 run on the tensor cores; other widths on the fp32 units.  q and cache bases and strides are multiples
  * of 16 bytes (CSA_ERR_MISALIGNED).  Products take bf16 operands (an 8-bit value is exact in bf16; its scale is
  * applied in fp32) and fp32 sums; on the tensor cores the weights exp(s - m) are rounded to bf16 for the second

@@ -93,6 +93,7 @@ class RMSNormFunction(torch.autograd.Function):
         return out, total
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_total):
         h, weight, rstd = ctx.saved_tensors
         if grad_out is None:  # only the sum was used

@@ -170,8 +170,8 @@ namespace csa {
 cudaError_t allow_max_smem(const void *fn)
 {
     static std::mutex mu;
-    static int devs[256];
-    static const void *fns[256];
+    static int devs[1024];
+    static const void *fns[1024];
     static int n = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -189,7 +189,7 @@ cudaError_t allow_max_smem(const void *fn)
     if (e == cudaSuccess)  // the device maximum less the kernel's static shared memory
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  optin - static_cast<int>(fa.sharedSizeBytes));
-    if (e == cudaSuccess && n < 256) {
+    if (e == cudaSuccess && n < 1024) {
         devs[n] = dev;
         fns[n] = fn;
         ++n;
@@ -215,10 +215,10 @@ cudaError_t cached_resident(const ResidentKey &k, int *resident, cudaError_t (*q
     static std::mutex mu;
     static ResidentKey keys[256];
     static int vals[256];
-    static int n = 0;
+    static int n = 0;  // entries so far; past 256 the oldest makes room
     {
         std::lock_guard<std::mutex> g(mu);
-        for (int i = 0; i < n; ++i)
+        for (int i = 0; i < (n < 256 ? n : 256); ++i)
             if (keys[i].dev == k.dev && keys[i].fn == k.fn && keys[i].threads == k.threads &&
                 keys[i].smem == k.smem && keys[i].cluster == k.cluster) {
                 *resident = vals[i];
@@ -229,11 +229,9 @@ cudaError_t cached_resident(const ResidentKey &k, int *resident, cudaError_t (*q
     if (e != cudaSuccess)
         return e;
     std::lock_guard<std::mutex> g(mu);
-    if (n < 256) {
-        keys[n] = k;
-        vals[n] = *resident;
-        ++n;
-    }
+    keys[n % 256] = k;
+    vals[n % 256] = *resident;
+    n = n + 1 < 512 ? n + 1 : 256;
     return cudaSuccess;
 }
 

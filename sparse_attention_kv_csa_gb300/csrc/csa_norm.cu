@@ -47,8 +47,12 @@ norm_fwd_kernel(const NormFwdParams p)
             return;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TEAM + t) * VEC;
-            if (c < p.dim) {
+            // short vectors: past the row's end the first one again, as a branch a load would serialise the loads
+            // (16394 rows of 4100: 303 us with, 140 without)
+            int c = (i * TEAM + t) * VEC;
+            if (VEC * sizeof(T) < 16)
+                c = c < p.dim ? c : 0;
+            if (VEC * sizeof(T) < 16 || c < p.dim) {
                 nx[i] = load<T, VEC>(x + row * p.x_stride + c);
                 if (res)
                     nr[i] = load<T, VEC>(res + row * p.residual_stride + c);
@@ -227,12 +231,16 @@ template <typename T, typename OUT> cudaError_t fwd_size(const NormFwdParams &p,
     if constexpr (sizeof(T) == 2)
         if (vec == 2) {
             if (p.dim <= 512) return fwd_go<T, OUT, 2, 32, 8>(p, st);
+            if (p.dim <= 1024) return fwd_go<T, OUT, 2, 64, 8>(p, st);
             if (p.dim <= 2048) return fwd_go<T, OUT, 2, 128, 8>(p, st);
+            if (p.dim <= 4096) return fwd_go<T, OUT, 2, 128, 16>(p, st);
             if (p.dim <= 8192) return fwd_go<T, OUT, 2, 256, 16>(p, st);
             return fwd_go<T, OUT, 2, 512, 16>(p, st);
         }
     if (p.dim <= 512) return fwd_go<T, OUT, 1, 32, 16>(p, st);
+    if (p.dim <= 1024) return fwd_go<T, OUT, 1, 64, 16>(p, st);
     if (p.dim <= 2048) return fwd_go<T, OUT, 1, 128, 16>(p, st);
+    if (p.dim <= 4096) return fwd_go<T, OUT, 1, 256, 16>(p, st);
     if (p.dim <= 8192) return fwd_go<T, OUT, 1, 512, 16>(p, st);
     return fwd_go<T, OUT, 1, 1024, 16>(p, st);
 }

@@ -53,8 +53,11 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
         x.rstd = __ldg(p.rstd + r);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TEAM + t) * VEC;
-            if (c < p.dim) {
+            // short vectors: past the row's end the first one again, as a branch a load would serialise the loads
+            int c = (i * TEAM + t) * VEC;
+            if (VEC * sizeof(T) < 16)
+                c = c < p.dim ? c : 0;
+            if (VEC * sizeof(T) < 16 || c < p.dim) {
                 x.h[i] = load<T, VEC>(h + r * p.h_stride + c);
                 x.g[i] = load<T, VEC>(dy + r * p.grad_out_stride + c);
                 if (dh)
@@ -231,13 +234,18 @@ cudaError_t bwd_size(const NormBwdParams &p, int vec, float *partial, int *block
     if constexpr (sizeof(T) == 2)
         if (vec == 2) {
             if (p.dim <= 512) return bwd_go<T, 2, 64, 4>(p, partial, blocks, plan, st);
+            if (p.dim <= 1024) return bwd_go<T, 2, 128, 4>(p, partial, blocks, plan, st);
             if (p.dim <= 2048) return bwd_go<T, 2, 256, 4>(p, partial, blocks, plan, st);
             if (p.dim <= 4096) return bwd_go<T, 2, 512, 4>(p, partial, blocks, plan, st);
+            if (p.dim <= 8192) return bwd_go<T, 2, 512, 8>(p, partial, blocks, plan, st);
             return bwd_go<T, 2, 1024, 8>(p, partial, blocks, plan, st);
         }
     if (p.dim <= 256) return bwd_go<T, 1, 32, 8>(p, partial, blocks, plan, st);
+    if (p.dim <= 512) return bwd_go<T, 1, 64, 8>(p, partial, blocks, plan, st);
+    if (p.dim <= 1024) return bwd_go<T, 1, 128, 8>(p, partial, blocks, plan, st);
     if (p.dim <= 2048) return bwd_go<T, 1, 256, 8>(p, partial, blocks, plan, st);
     if (p.dim <= 4096) return bwd_go<T, 1, 512, 8>(p, partial, blocks, plan, st);
+    if (p.dim <= 8192) return bwd_go<T, 1, 1024, 8>(p, partial, blocks, plan, st);
     return bwd_go<T, 1, 1024, 16>(p, partial, blocks, plan, st);
 }
 

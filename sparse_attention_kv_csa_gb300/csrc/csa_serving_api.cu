@@ -203,9 +203,9 @@ int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     if (n_heads > 4096 || n_tokens * (int64_t)n_heads >= (int64_t(1) << 31) || n_req > csa::kMaxRequests)
         return fail_status(CSA_ERR_TOO_LARGE, "n_heads <= 4096, n_tokens * n_heads < 2^31 and n_req <= %d (got %d, %lld, %d)",
                            csa::kMaxRequests, n_heads, (long long)n_tokens, n_req);
-    if (n_pages >= (int64_t(1) << 31) || (int64_t)width * page_size >= (int64_t(1) << 31) ||
-        n_pages * page_size >= (int64_t(1) << 31))
-        return fail_status(CSA_ERR_TOO_LARGE, "n_pages * page_size and width * page_size must be below 2^31");
+    constexpr int64_t kMostRows = (int64_t(1) << 31) - 128;  // (row numbers are rounded up to whole tiles in 32 bits)
+    if (n_pages > kMostRows || (int64_t)width * page_size > kMostRows || n_pages * page_size > kMostRows)
+        return fail_status(CSA_ERR_TOO_LARGE, "n_pages * page_size and width * page_size must be at most 2^31 - 128");
     CSA_TRY(check_stride(q_head_stride, head_dim, "q_head_stride"));
     CSA_TRY(check_stride(q_token_stride, head_dim, "q_token_stride"));
     CSA_TRY(check_stride(cache_stride, head_dim, "cache_stride"));
