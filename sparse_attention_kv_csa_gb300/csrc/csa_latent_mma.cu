@@ -234,6 +234,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         for (int i = 0; i < stages; ++i) {
             mbar_init(smem_addr(&s.kv_full[i]), ROWS == kTma ? 1 : kGroups);
             mbar_init(smem_addr(&s.kv_empty[i]), 1);
+            *reinterpret_cast<uint64_t *>(s.missing[i]) = 0;
         }
         for (int i = 0; i < kScores; ++i)
             mbar_init(smem_addr(&s.s_full[i]), 1);
@@ -893,6 +894,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         const uint32_t kv_smem = smem_addr(kv_mem);
         const int none = (int)(p.n_pages * p.page_size / 8);  // a group past the end reads as zeros
         const int copies = kGroups / plan.box_groups;
+        uint32_t dirty = 0;  // stages whose flags are not all clear
         int tile = 0;
         Walk<R> w(p, s, units);
         while (ok && w.next()) {
@@ -908,21 +910,25 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 const uint32_t missing = __ballot_sync(~0u, need && !found) & 0xffu;
                 const int at = need && found ? (next * p.page_size + (int)p.by_page.remainder(t * R + (lane & 7) * 8)) >> 3 : none;
                 next = look_up(t + 1);
+                // all that can be is found before the wait
+                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * kTileBytes;
+                const bool plain = !missing && (t + 1) * R <= end;  // runs of groups that lie together
+                const int first = __shfl_sync(~0u, at, plain ? (lane & 7) * plan.box_groups & 7 : lane & 7);
                 if (tile >= stages) {
                     ok = mbar_wait(smem_addr(&s.kv_empty[st]), (tile / stages - 1) & 1, status);
                     ok = __all_sync(~0u, ok);
                     if (!ok)
                         break;
                 }
-                const uint32_t bar = smem_addr(&s.kv_full[st]), dst = kv_smem + st * kTileBytes;
-                if (lane < 8)
-                    s.missing[st][lane] = missing >> lane & 1 ? 0xff : 0;
-                __syncwarp();
+                if (missing || dirty >> st & 1) {
+                    if (lane < 8)
+                        s.missing[st][lane] = missing >> lane & 1 ? 0xff : 0;
+                    dirty = missing ? dirty | 1u << st : dirty & ~(1u << st);
+                    __syncwarp();
+                }
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar, kTileBytes);
                 __syncwarp();
-                const bool plain = !missing && (t + 1) * R <= end;  // runs of groups that lie together
-                const int first = __shfl_sync(~0u, at, plain ? (lane & 7) * plan.box_groups & 7 : lane & 7);
                 if (plain ? lane < copies : lane < kGroups)
                     tma_load_4d(dst + lane * (plain ? plan.box_groups : 1) * kGroupBytes, plain ? &boxes : &groups, 0, 0, 0, first, bar);
             }
