@@ -12,7 +12,7 @@
 //   dw_j = sum over rows of dy_j h_j rstd
 //
 // Both are bound by DRAM: every array is read or written once and a row stays in registers between its sums and its
-// output.  A row belongs to one team of 32 to 1024 threads; a block holds one team (or several small ones) and walks
+// output.  A row belongs to one team of 16 to 1024 threads; a block holds one team (or several small ones) and walks
 // the rows with the grid's stride, its weights in registers.  Rows of 16-byte vectors for teams of 128 threads or more
 // come by bulk copies into a ring of rows in shared memory, several rows ahead (loads into registers a row ahead kept
 // too few bytes on the way: 130 against 95 us for 16411 rows of 4096 with 8-bit output); other rows are loaded into
@@ -174,7 +174,7 @@ template <int VEC> __device__ __forceinline__ float2 dot_add(const float (&a)[VE
 template <int TEAM, bool MAX> __device__ __forceinline__ float team_reduce(float v, float *buf)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
+    for (int o = TEAM < 32 ? TEAM / 2 : 16; o; o >>= 1) {
         const float u = __shfl_xor_sync(~0u, v, o);
         v = MAX ? max_nan(v, u) : v + u;
     }

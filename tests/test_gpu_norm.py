@@ -171,3 +171,28 @@ def test_side_stream_and_graph():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o[0], want[0]) and torch.equal(d[0], grads[0]) and torch.equal(d[1], grads[1])
+
+
+@pytest.mark.parametrize("dim,bits8,group,dtype",
+                         [(128, False, 0, torch.bfloat16), (128, True, 0, torch.bfloat16), (136, False, 0, torch.float16),
+                          (256, True, 128, torch.bfloat16), (512, True, 0, torch.bfloat16), (512, True, 128, torch.float16),
+                          (504, True, 0, torch.bfloat16), (128, True, 128, torch.float32), (256, True, 128, torch.float32),
+                          (256, False, 0, torch.float32), (33, False, 0, torch.bfloat16), (576, True, 0, torch.bfloat16)])
+def test_many_narrow_rows(dim, bits8, group, dtype):
+    # two rows a warp, where 16-bit types and whole vectors allow it
+    n = 33001
+    x, r, w = rand((n, dim), dtype, 20), rand((n, dim), dtype, 21), rand((dim,), torch.float32, 22)
+    x[17], r[17] = 0, 0
+    out, scales, total, rstd = csa.rms_norm_forward(x, w, 1e-6, residual=r, scale_group=group,
+                                                    out_dtype=torch.float8_e4m3fn if bits8 else None)
+    h, y, rs = u.norm64(x, w, 1e-6, r)
+    e = (dim / 2 + 16) * U
+    assert torch.equal(total, h) and ((rstd.double() - rs).abs() <= e * rs).all()
+    if not bits8:
+        assert ((out.double() - y).abs() <= (u.HALF[dtype] + 2 * e) * y.abs() + (2.0 ** -25 if dtype == torch.float16 else 0)).all()
+        return
+    groups = y.view(n, -1, group or dim)
+    want = groups.abs().amax(2) / 448
+    assert ((scales.double() - want).abs() <= e * want).all()
+    got = out.double().view_as(groups) * scales.double()[..., None]
+    assert ((got - groups).abs() <= (2.0 ** -4 + 2 * e) * groups.abs() + (2.0 ** -10 + 2 * e) * want[..., None]).all()
