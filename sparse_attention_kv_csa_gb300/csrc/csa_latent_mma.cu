@@ -354,6 +354,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         if (tid == 0)
             s.total = total;
     }
+    // TMA copies and the tensor core take over the space that these sums were in
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
