@@ -64,22 +64,20 @@ norm_fwd_kernel(const NormFwdParams p)
     if (STAGED && t == 0)
         for (int i = 0; i < ring.stages; ++i)
             refill(row + i * step, i);
-    int stage = 0;
-    uint32_t phase = 0;
+    RingAt at;
     for (int64_t it = 0; it < passes; ++it, row += step) {
         const bool live = row < p.n_rows;
         float h[NV][VEC];
         float2 ss2 = splat(0.0f);
         if (STAGED && live) {
-            // (a wait that gives up sets the device's status word; the rows' results are then wrong, as documented)
-            mbar_wait(smem_addr(full + stage), phase, ring.status);
+            ring.wait(at, t == 0, row, step, p.n_rows);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TEAM + t) * VEC;
                 if (c < p.dim) {
-                    nx[i] = from_ring<T, VEC>(ring.at(stage, 0), c);
+                    nx[i] = from_ring<T, VEC>(ring.at(at.stage, 0), c);
                     if (res)
-                        nr[i] = from_ring<T, VEC>(ring.at(stage, 1), c);
+                        nr[i] = from_ring<T, VEC>(ring.at(at.stage, 1), c);
                 }
             }
         }
@@ -112,12 +110,9 @@ norm_fwd_kernel(const NormFwdParams p)
             // the sum's barrier: the whole team has read the stage
             if (TEAM <= 32)
                 __syncwarp();
-            if (t == 0)
-                refill(row + ring.stages * step, stage);
-            if (++stage == ring.stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            if (t == 0 && at.ok)
+                refill(row + ring.stages * step, at.stage);
+            ring.next(at);
         }
         const float rstd = 1.0f / sqrtf(fmaf(ss, inv_dim, p.eps));
         int64_t to = row;

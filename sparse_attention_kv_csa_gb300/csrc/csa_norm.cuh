@@ -27,6 +27,7 @@
 
 #include "csa_device.cuh"
 #include "csa_launch.h"
+#include "csa_norm_ring.cuh"
 #include "csa_serving_launch.h"
 
 namespace csa {
@@ -191,36 +192,6 @@ template <int TEAM, bool MAX> __device__ __forceinline__ float team_reduce(float
     }
     return v;
 }
-
-// A team's ring of rows in shared memory: the arrays' rows side by side, refilled by the team's first thread once the
-// team has read them.
-struct Ring {
-    uint8_t *mem;
-    uint64_t *full;
-    int stages, row_bytes, arrays;
-    unsigned *status;
-    __device__ void init(bool first) const
-    {
-        if (first) {
-            for (int i = 0; i < stages; ++i)
-                mbar_init(smem_addr(full + i), 1);
-            mbar_init_fence();
-        }
-        __syncthreads();
-    }
-    __device__ void fill(int stage, const void *a, const void *b, const void *c) const
-    {
-        const uint32_t bar = smem_addr(full + stage), dst = smem_addr(mem) + stage * arrays * row_bytes;
-        mbar_arrive_expect_tx(bar, arrays * row_bytes);
-        bulk_g2s(dst, a, row_bytes, bar);
-        if (b)
-            bulk_g2s(dst + row_bytes, b, row_bytes, bar);
-        if (c)
-            bulk_g2s(dst + (arrays - 1) * row_bytes, c, row_bytes, bar);
-    }
-    __device__ const uint8_t *at(int stage, int array) const { return mem + (stage * arrays + array) * row_bytes; }
-};
-constexpr int kMaxRing = 8;
 
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> from_ring(const uint8_t *row, int c)
 {

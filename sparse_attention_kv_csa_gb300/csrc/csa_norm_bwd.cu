@@ -87,22 +87,21 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
     } else if (kRoomy) {
         fetch(row, next);
     }
-    int stage = 0;
-    uint32_t phase = 0;
+    RingAt at;
     for (int64_t it = 0; it < passes; ++it, row += step) {
         const bool live = row < p.n_rows;
         if (STAGED) {
             if (live) {
                 now.rstd = __ldg(p.rstd + row);
-                mbar_wait(smem_addr(full + stage), phase, ring.status);
+                ring.wait(at, t == 0, row, step, p.n_rows);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = (i * TEAM + t) * VEC;
                     if (c < p.dim) {
-                        now.h[i] = from_ring<T, VEC>(ring.at(stage, 0), c);
-                        now.g[i] = from_ring<T, VEC>(ring.at(stage, 1), c);
+                        now.h[i] = from_ring<T, VEC>(ring.at(at.stage, 0), c);
+                        now.g[i] = from_ring<T, VEC>(ring.at(at.stage, 1), c);
                         if (dh)
-                            now.r[i] = from_ring<T, VEC>(ring.at(stage, 2), c);
+                            now.r[i] = from_ring<T, VEC>(ring.at(at.stage, 2), c);
                     }
                 }
             }
@@ -128,12 +127,9 @@ norm_bwd_kernel(const NormBwdParams p, float *__restrict__ partial)
         if (STAGED) {
             if (TEAM == 32)
                 __syncwarp();
-            if (t == 0)
-                refill(row + ring.stages * step, stage);
-            if (++stage == ring.stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            if (t == 0 && at.ok)
+                refill(row + ring.stages * step, at.stage);
+            ring.next(at);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
