@@ -74,8 +74,8 @@ CSA_API int csa_rms_norm_bwd(const void *h, int64_t h_stride, const void *grad_o
  *   counts    [4]             new rows, pages taken, pages short, the most pages that a request needs
  * taken: device int32 or NULL, the entries of free_pages [n_free] that are already used.  table: [n_req, width] with
  * row stride table_stride; table_out is contiguous and may be table itself when table_stride == width.  All arrays
- * are int32 unless said otherwise.  Negative lengths count as 0.  n_req <= 14000; the total of new rows must stay
- * below 2^31.
+ * are int32 unless said otherwise.  Negative lengths count as 0.  n_req <= 14000.  Sums of rows and of pages are held at
+ * 2^31 - 1.
  */
 CSA_API int csa_page_tables(const int32_t *before, const int32_t *after, int32_t n_req, int32_t ratio, int32_t page_size,
                     const int32_t *free_pages, int32_t n_free, const int32_t *taken, const int32_t *table,

@@ -32,6 +32,9 @@ __device__ __forceinline__ Req request(const PageParams &p, int r)
     return q;
 }
 
+// a + b of two counts, held at 2^31 - 1: in any order the same, and no offset formed of such sums goes astray.
+__device__ __forceinline__ int sum(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
 __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams p)
 {
     extern __shared__ int sums[];
@@ -46,14 +49,14 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams 
         widest = 0;
     __syncthreads();
     // Exclusive prefix sums: a thread adds up a stretch of requests, the threads' sums are scanned, the thread goes over
-    // its stretch again.  All sums are of whole numbers, so any order gives the same.
+    // its stretch again.
     const int per = (n + kThreads - 1) / kThreads, lo = min(n, tid * per), hi = min(n, lo + per);
     int rows = 0, pages = 0, wide = 0;
 #pragma unroll 4
     for (int r = lo; r < hi; ++r) {
         const Req q = request(p, r);
-        rows += q.new_rows - q.old_rows;
-        pages += q.need - q.held;
+        rows = sum(rows, q.new_rows - q.old_rows);
+        pages = sum(pages, q.need - q.held);
         wide = max(wide, q.need);
     }
     int a = rows, b = pages;
@@ -61,8 +64,8 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams 
     for (int o = 1; o < 32; o <<= 1) {
         const int ua = __shfl_up_sync(~0u, a, o), ub = __shfl_up_sync(~0u, b, o);
         if (lane >= o) {
-            a += ua;
-            b += ub;
+            a = sum(a, ua);
+            b = sum(b, ub);
         }
     }
     if (lane == 31) {
@@ -71,24 +74,26 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageParams 
     }
     __syncthreads();
     int base_rows = 0, base_pages = 0;
-    a -= rows;
-    b -= pages;
+    a = __shfl_up_sync(~0u, a, 1);
+    b = __shfl_up_sync(~0u, b, 1);
+    if (lane == 0)
+        a = b = 0;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
         const int pa = part[0][i], pb = part[1][i];
         if (i < warp) {
-            a += pa;
-            b += pb;
+            a = sum(a, pa);
+            b = sum(b, pb);
         }
-        base_rows += pa;
-        base_pages += pb;
+        base_rows = sum(base_rows, pa);
+        base_pages = sum(base_pages, pb);
     }
     for (int r = lo; r < hi; ++r) {
         const Req q = request(p, r);
         cu_rows[r] = a;
         cu_pages[r] = b;
-        a += q.new_rows - q.old_rows;
-        b += q.need - q.held;
+        a = sum(a, q.new_rows - q.old_rows);
+        b = sum(b, q.need - q.held);
     }
     if (tid == 0) {
         cu_rows[n] = base_rows;
