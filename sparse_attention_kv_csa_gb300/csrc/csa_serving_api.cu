@@ -200,7 +200,7 @@ int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
         return fail_status(CSA_ERR_UNSUPPORTED, "cache_dtype must be bf16 or e4m3 (got %d)", cache_dtype);
     if (!(scale > 0.0f) || !(scale < 3.0e38f))
         return fail_status(CSA_ERR_INVALID_VALUE, "scale must be positive and finite (got %g)", (double)scale);
-    if (n_heads > 4096 || n_tokens * (int64_t)n_heads >= (int64_t(1) << 31) || n_req > csa::kMaxRequests)
+    if (n_heads > 4096 || n_tokens >= (int64_t(1) << 31) || n_tokens * (int64_t)n_heads >= (int64_t(1) << 31) || n_req > csa::kMaxRequests)
         return fail_status(CSA_ERR_TOO_LARGE, "n_heads <= 4096, n_tokens * n_heads < 2^31 and n_req <= %d (got %d, %lld, %d)",
                            csa::kMaxRequests, n_heads, (long long)n_tokens, n_req);
     constexpr int64_t kMostRows = (int64_t(1) << 31) - 128;  // (row numbers are rounded up to whole tiles in 32 bits)
