@@ -25,12 +25,14 @@ norm_fwd_kernel(const NormFwdParams p)
     pdl_trigger();
     const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
     float w[NV][VEC];
+    bool odd_weight = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int c = (i * TEAM + t) * VEC + k;
             w[i][k] = c < p.dim ? (p.weight ? __ldg(p.weight + c) : 1.0f) : 0.0f;
+            odd_weight |= !(fabsf(w[i][k]) < INFINITY);
         }
     // 128 columns lie in 128 / VEC neighbouring lanes; the host takes that form with whole vectors only
     const bool grouped = VEC * sizeof(T) == 16 && p.scale_group == 128;
@@ -124,8 +126,9 @@ norm_fwd_kernel(const NormFwdParams p)
         }
         const bool write = live && to >= 0 && to < p.n_slots;
         float amax = 0.0f;
-        // (a NaN among the y needs a sum that is not finite; the plain maximum drops NaN)
-        const bool odd = !(ss < INFINITY);
+        // The plain maximum drops NaN.  A NaN among the y needs a sum that is not finite, a zero row without eps (0 times
+        // an infinite rstd) or a weight that is not finite.
+        const bool odd = !(ss < INFINITY) || !(rstd < INFINITY) || odd_weight;
         auto magnitude = [&](int i, float m) {
             if (odd) {
 #pragma unroll

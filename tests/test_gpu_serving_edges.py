@@ -37,3 +37,44 @@ def test_page_totals_past_31_bits_are_held(n):
     assert table.tolist() == want and cu.tolist() == list(range(n)) + [most]
     assert slots.tolist() == [1000 + i for i in range(n + 3)] + [-1, -1]
     assert counts.tolist() == [most, n + 3, most - n - 3, most]
+
+
+# (narrow and wide teams, odd widths, two rows a warp, and rows enough for the ring)
+NORMS = [(5, 512, 0, torch.bfloat16), (5, 512, 128, torch.bfloat16), (3, 1001, 0, torch.float16), (4, 4096, 128, torch.float32),
+         (33001, 128, 0, torch.bfloat16), (33001, 256, 128, torch.float16), (4000, 4096, 128, torch.bfloat16),
+         (4000, 2048, 0, torch.float32)]
+
+
+@pytest.mark.parametrize("n,dim,group,dtype", NORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_weights_that_are_not_finite_reach_the_scales_of_eight_bits(n, dim, group, dtype, bad):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((n, dim), device="cuda", generator=g).to(dtype)
+    w = torch.rand(dim, device="cuda", generator=g) + 0.5
+    clean, clean_scales, _, _ = csa.rms_norm_forward(x, w, out_dtype=torch.float8_e4m3fn, scale_group=group)
+    col = dim - 3
+    x[n - 1, col] = 0  # an infinite weight times 0
+    w[col] = bad
+    out, scales, _, _ = csa.rms_norm_forward(x, w, out_dtype=torch.float8_e4m3fn, scale_group=group)
+    x64 = x.double()
+    y = x64 * (x64.square().mean(1, keepdim=True) + 1e-6).rsqrt() * w.double()
+    want = y.view(n, -1, group or dim).abs().amax(2)  # NaN where there is one, else infinite
+    hit = ~want.isfinite()
+    assert hit.any(1).all()
+    assert torch.equal(scales.isnan(), want.isnan()) and torch.equal(scales.isinf(), want.isinf())
+    # the groups without that column stay as they were
+    same = ~hit & (torch.arange(n, device="cuda") < n - 1)[:, None]
+    assert torch.equal(scales[same], clean_scales[same])
+    bytes_of = lambda t: t.view(torch.uint8).view(n, -1, group or dim)[same]  # noqa: E731
+    assert torch.equal(bytes_of(out), bytes_of(clean))
+
+
+@pytest.mark.parametrize("n,dim,group,dtype", NORMS)
+def test_rows_of_zeros_without_eps(n, dim, group, dtype):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((n, dim), device="cuda", generator=g).to(dtype)
+    x[n // 2] = 0
+    out, scales, _, rstd = csa.rms_norm_forward(x, None, 0.0, out_dtype=torch.float8_e4m3fn, scale_group=group)
+    assert rstd[n // 2].isinf() and scales[n // 2].isnan().all() and out[n // 2].float().isnan().all()
+    rest = torch.arange(n, device="cuda") != n // 2
+    assert scales[rest].isfinite().all() and rstd[rest].isfinite().all() and out[rest].float().isfinite().all()
