@@ -85,10 +85,19 @@ def _empty(shape, dtype, device, stream):
         return _torch.empty(shape, dtype=dtype, device=device)
 
 
+def _fit(bits, **numbers):
+    """The numbers fit the entry points' integers (ctypes would cut them off silently)."""
+    for name, v in numbers.items():
+        if not -1 << (bits - 1) <= v < 1 << (bits - 1):
+            raise ValueError("%s must fit %d bits (got %s)" % (name, bits, v))
+
+
 # ------------------------------------------------------------ the C entry points
 
 def csa_rms_norm_fwd(x, x_stride, residual, residual_stride, weight, n_rows, dim, eps, dtype, slots, n_slots, out,
                      out_stride, out_dtype, scales, scale_group, residual_out, rstd, stream=None) -> None:
+    _fit(32, dim=dim, dtype=dtype, out_dtype=out_dtype, scale_group=scale_group)
+    _fit(64, x_stride=x_stride, residual_stride=residual_stride, n_rows=n_rows, n_slots=n_slots, out_stride=out_stride)
     _raise(_lib.csa_rms_norm_fwd(_addr(x), x_stride, _addr(residual), residual_stride, _addr(weight), n_rows, dim, eps,
                                  dtype, _addr(slots), n_slots, _addr(out), out_stride, out_dtype, _addr(scales),
                                  scale_group, _addr(residual_out), _addr(rstd), _stream(stream)))
@@ -96,6 +105,8 @@ def csa_rms_norm_fwd(x, x_stride, residual, residual_stride, weight, n_rows, dim
 
 def csa_rms_norm_bwd(h, h_stride, grad_out, grad_out_stride, grad_residual, grad_residual_stride, weight, rstd, n_rows,
                      dim, dtype, grad_x, grad_weight, stream=None) -> None:
+    _fit(32, dim=dim, dtype=dtype)
+    _fit(64, h_stride=h_stride, grad_out_stride=grad_out_stride, grad_residual_stride=grad_residual_stride, n_rows=n_rows)
     _raise(_lib.csa_rms_norm_bwd(_addr(h), h_stride, _addr(grad_out), grad_out_stride, _addr(grad_residual),
                                  grad_residual_stride, _addr(weight), _addr(rstd), n_rows, dim, dtype, _addr(grad_x),
                                  _addr(grad_weight), _stream(stream)))
@@ -103,6 +114,8 @@ def csa_rms_norm_bwd(h, h_stride, grad_out, grad_out_stride, grad_residual, grad
 
 def csa_page_tables(before, after, n_req, ratio, page_size, free_pages, n_free, taken, table, table_stride, width,
                     capacity, table_out, cu_rows, slots, counts, stream=None) -> None:
+    _fit(32, n_req=n_req, ratio=ratio, page_size=page_size, n_free=n_free, width=width)
+    _fit(64, table_stride=table_stride, capacity=capacity)
     _raise(_lib.csa_page_tables(_addr(before), _addr(after), n_req, ratio, page_size, _addr(free_pages), n_free,
                                 _addr(taken), _addr(table), table_stride, width, capacity, _addr(table_out),
                                 _addr(cu_rows), _addr(slots), _addr(counts), _stream(stream)))
@@ -111,6 +124,10 @@ def csa_page_tables(before, after, n_req, ratio, page_size, free_pages, n_free, 
 def csa_latent_attention(q, q_token_stride, q_head_stride, cu_q, n_req, n_tokens, n_heads, head_dim, v_dim, cache,
                          cache_stride, cache_dtype, row_scales, n_pages, page_size, block_table, table_stride, width,
                          seq_lens, ratio, scale, sink, out, lse, stream=None) -> None:
+    _fit(32, n_req=n_req, n_heads=n_heads, head_dim=head_dim, v_dim=v_dim, cache_dtype=cache_dtype, page_size=page_size,
+         width=width, ratio=ratio)
+    _fit(64, q_token_stride=q_token_stride, q_head_stride=q_head_stride, n_tokens=n_tokens, cache_stride=cache_stride,
+         n_pages=n_pages, table_stride=table_stride)
     _raise(_lib.csa_latent_attention(_addr(q), q_token_stride, q_head_stride, _addr(cu_q), n_req, n_tokens, n_heads,
                                      head_dim, v_dim, _addr(cache), cache_stride, cache_dtype, _addr(row_scales),
                                      n_pages, page_size, _addr(block_table), table_stride, width, _addr(seq_lens),
@@ -215,6 +232,7 @@ def rms_norm_forward(x, weight=None, eps=1e-6, residual=None, out_dtype=None, sc
             return r if type(r) is tuple else _raise(r)
     shape, code, d = _matrix("x", x)
     n, dim = shape
+    _fit(32, dim=dim)
     dtype, device, f32 = x.dtype, x.device, _torch.float32
     xs = dim if x.is_contiguous() else _rows("x", x, dtype, shape, d)
     rs = 0 if residual is None else _rows("residual", residual, dtype, shape, d)
@@ -269,6 +287,7 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, stream=None
             return r if type(r) is tuple else _raise(r)
     shape, code, d = _matrix("h", h)
     n, dim = shape
+    _fit(32, dim=dim)
     dtype, device, f32 = h.dtype, h.device, _torch.float32
     hs = dim if h.is_contiguous() else _rows("h", h, dtype, shape, d)
     gs = _rows("grad_out", grad_out, dtype, shape, d)
@@ -300,6 +319,7 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
         r = _short.page_tables(before, after, ratio, page_size, free_pages, block_table, capacity, taken, out)
         if r is not None:
             return r if type(r) is tuple else _raise(r)
+    _fit(32, ratio=ratio, page_size=page_size)
     i32 = _torch.int32
     if not isinstance(before, _torch.Tensor):
         raise TypeError("before must be a tensor")
@@ -310,6 +330,7 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
     if taken is not None:
         _check("taken", taken, i32, (1,), d)
     stride, width = _table("block_table", block_table, n, d)
+    _fit(32, n_req=n, n_free=n_free, width=width)
     if capacity < 0:
         raise ValueError("capacity must be >= 0 (got %s)" % (capacity,))
     if out is None:
@@ -342,6 +363,7 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
         r = _short.latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim, row_scales, sink, out)
         if r is not None:
             return r if type(r) is tuple else _raise(r)
+    _fit(32, ratio=ratio, v_dim=0 if v_dim is None else v_dim)
     bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
     if type(q) is not _Tensor or q.dtype is not bf16 or q.dim() != 3:
         _fits("q", q, bf16, (None, None, None), None)
@@ -375,6 +397,7 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
         raise ValueError("cu_q must be [n_req + 1]")
     _check("seq_lens", seq_lens, i32, (n_req,), d)
     stride, width = _table("block_table", block_table, n_req, d)
+    _fit(32, n_req=n_req, n_heads=heads, head_dim=dim, page_size=page_size, width=width)
     if sink is not None:
         _check("sink", sink, f32, (heads,), d)
     v_dim = dim if v_dim is None else v_dim
