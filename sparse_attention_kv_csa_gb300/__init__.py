@@ -59,7 +59,7 @@ class _Grouping(ctypes.Structure):
 
 
 def _load():
-    path = _build.build()  # no-op when up to date
+    path = _build.build_library()  # no-op when up to date
     lib = ctypes.CDLL(path)
     P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     common = [P, P, P, P, P, i32, i32, i32, i32, i32]

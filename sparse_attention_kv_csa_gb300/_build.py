@@ -2,8 +2,9 @@
 
 Each .cu file compiles to an object in parallel, then one shared-library link.
 The build is skipped when the library is newer than every source and header.
-csa_torch, the serving helpers' way from tensors to the library, is a CPython
-extension against torch's headers, compiled beside it (no CUDA code of its own).
+csa_torch, the serving helpers' short way from tensors to the library, is a CPython
+extension against torch's headers (no CUDA code of its own), compiled beside it by
+build() or on the helpers' first call; they do without where it cannot be had.
 """
 from __future__ import annotations
 
@@ -88,18 +89,18 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile libcsa.so (and csa_torch.so beside it, where torch is) if missing or stale; returns libcsa's path."""
+    """Compile libcsa.so, and csa_torch.so beside it where torch is, if missing or stale; returns libcsa's path."""
     pending = None
     if _torch_dir() is not None and (force or binding_stale()):
         pending = cf.ThreadPoolExecutor(max_workers=1).submit(build_binding, force)
-    try:
-        return _build_library(force, verbose, ptxas_info)
-    finally:
-        if pending is not None:
-            pending.result()
+    path = build_library(force, verbose, ptxas_info)
+    if pending is not None:
+        pending.result()
+    return path
 
 
-def _build_library(force: bool, verbose: bool, ptxas_info: bool) -> str:
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile libcsa.so if missing or stale (all that importing the package needs); returns its path."""
     if not force and not stale():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import warnings
 
 from . import _build
 
@@ -26,7 +27,7 @@ _raise = None
 _torch = None
 _Tensor = None
 _raw_stream = None
-_short = None  # csa_torch: the ordinary case of each helper in one call
+_short = None  # csa_torch: the ordinary case of each helper in one call (None where it is not to be had)
 _e4m3 = None
 
 BF16, F16, F32, E4M3 = 0, 1, 2, 3
@@ -51,12 +52,17 @@ def _load_torch():
     """torch is imported on first use, like in the rest of the package."""
     global _torch, _Tensor, _raw_stream, _short, _e4m3
     import torch
-    spec = importlib.util.spec_from_file_location("csa_torch", _build.build_binding())
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
-                  ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention")))
-    _short, _e4m3 = module, torch.float8_e4m3fn
+    try:
+        spec = importlib.util.spec_from_file_location("csa_torch", _build.build_binding())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
+                      ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention")))
+        _short = module
+    except Exception as e:  # no compiler or headers, or a library that this torch does not load
+        warnings.warn("csa_torch is not to be had (%s): calls are checked and made in Python, some 8 us longer each"
+                      % (str(e) or type(e).__name__).splitlines()[0], RuntimeWarning, stacklevel=3)
+    _e4m3 = torch.float8_e4m3fn
     _torch, _Tensor = torch, torch.Tensor
     # the current stream's handle without building a Stream object (some 3 us of a call of 10)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -225,7 +231,7 @@ def rms_norm_forward(x, weight=None, eps=1e-6, residual=None, out_dtype=None, sc
     """
     if _torch is None:
         _load_torch()
-    if stream is None and (out_dtype is None or out_dtype is _e4m3):
+    if _short is not None and stream is None and (out_dtype is None or out_dtype is _e4m3):
         bits8 = out_dtype is _e4m3 or (out is not None and getattr(out, "dtype", None) is _e4m3)
         r = _short.rms_norm_forward(x, weight, eps, residual, bits8, scale_group, slots, out, scales)
         if r is not None:
@@ -281,7 +287,7 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, stream=None
     """
     if _torch is None:
         _load_torch()
-    if stream is None:
+    if _short is not None and stream is None:
         r = _short.rms_norm_backward(grad_out, h, weight, rstd, grad_residual)
         if r is not None:
             return r if type(r) is tuple else _raise(r)
@@ -315,7 +321,7 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
     """
     if _torch is None:
         _load_torch()
-    if stream is None:
+    if _short is not None and stream is None:
         r = _short.page_tables(before, after, ratio, page_size, free_pages, block_table, capacity, taken, out)
         if r is not None:
             return r if type(r) is tuple else _raise(r)
@@ -359,7 +365,7 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
     """
     if _torch is None:
         _load_torch()
-    if stream is None:
+    if _short is not None and stream is None:
         r = _short.latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim, row_scales, sink, out)
         if r is not None:
             return r if type(r) is tuple else _raise(r)

@@ -78,3 +78,29 @@ def test_rows_of_zeros_without_eps(n, dim, group, dtype):
     assert rstd[n // 2].isinf() and scales[n // 2].isnan().all() and out[n // 2].float().isnan().all()
     rest = torch.arange(n, device="cuda") != n // 2
     assert scales[rest].isfinite().all() and rstd[rest].isfinite().all() and out[rest].float().isfinite().all()
+
+
+def test_helpers_without_csa_torch_give_the_same(monkeypatch):
+    from sparse_attention_kv_csa_gb300 import serving
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((50, 128), device="cuda", generator=g).bfloat16()
+    w = torch.rand(128, device="cuda", generator=g)
+    cache = torch.randn((6, 16, 128), device="cuda", generator=g).bfloat16()
+    scales = torch.rand((6, 16), device="cuda", generator=g)
+    q = torch.randn((3, 8, 128), device="cuda", generator=g).bfloat16()
+    table, cu, lens = i32([[4, 1, -1], [0, 2, 5]]), i32([0, 1, 3]), i32([20, 48])
+
+    def calls():
+        a = csa.rms_norm_forward(x, w, residual=x)
+        b = csa.rms_norm_forward(x, w, out_dtype=torch.float8_e4m3fn, scale_group=128)
+        c = csa.rms_norm_backward(x, x, w, a[3], grad_residual=x)
+        d = csa.page_tables(i32([0, 9]), i32([70, 30]), 4, 4, i32(list(range(9))), i32([[7] * 5] * 2), 30)
+        e = csa.latent_attention(q, cache, table, cu, lens, 1, 0.1)
+        f = csa.latent_attention(q, cache.to(torch.float8_e4m3fn), table, cu, lens, 1, 0.1, 64, scales, torch.zeros(8, device="cuda"))
+        return [t if t is None or t.dtype != torch.float8_e4m3fn else t.view(torch.uint8) for r in (a, b, c, d, e, f) for t in r]
+
+    short = calls()
+    assert serving._short is not None
+    monkeypatch.setattr(serving, "_short", None)
+    for s, p in zip(short, calls()):
+        assert (s is None and p is None) or torch.equal(s, p)
