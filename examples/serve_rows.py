@@ -34,6 +34,7 @@ class Server:
         self.scales = torch.zeros((pages, page_size), device="cuda")
         self.free = torch.randperm(pages, device="cuda", generator=g).int()
         self.taken = torch.zeros(1, dtype=torch.int32, device="cuda")
+        # (as wide as the pool, so no request needs more columns)
         self.table = torch.full((requests, pages), -1, dtype=torch.int32, device="cuda")
         self.lens = [0] * requests  # tokens so far
         self.tail = [None] * requests  # kv and score from the block before the open one on

@@ -74,7 +74,10 @@ CSA_API int csa_rms_norm_bwd(const void *h, int64_t h_stride, const void *grad_o
  *   counts    [4]             new rows, pages taken, pages short, the most pages that a request needs
  * taken: device int32 or NULL, the entries of free_pages [n_free] that are already used.  table: [n_req, width] with
  * row stride table_stride; table_out is contiguous and may be table itself when table_stride == width.  All arrays
- * are int32 unless said otherwise.  Negative lengths count as 0.  n_req <= 14000.  Sums of rows and of pages are held at
+ * are int32 unless said otherwise.  A table narrower than a need (counts[3] > width) holds none of the pages past its
+ * columns, although counts[1] counts them and later requests get the entries of free_pages behind them: such a result is
+ * not to be kept.  Call again with a table of counts[3] columns or more (those past the pages that a request holds may
+ * have anything in them) and the same taken, which gives what the wider table would have given at once, after a call in place too.  Negative lengths count as 0.  n_req <= 14000.  Sums of rows and of pages are held at
  * 2^31 - 1.
  */
 CSA_API int csa_page_tables(const int32_t *before, const int32_t *after, int32_t n_req, int32_t ratio, int32_t page_size,

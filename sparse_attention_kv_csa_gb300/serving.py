@@ -317,7 +317,8 @@ def page_tables(before, after, ratio, page_size, free_pages, block_table, capaci
     used; block_table int32 [n_req, width]; capacity: how many slots to return.  ``out``: where the new table goes
     (block_table itself for an update in place), a new tensor by default.
     Returns (table, cu_rows int32 [n_req + 1], slots int64 [capacity], counts int32 [4]: new rows, pages taken, pages
-    short, pages of the widest request).
+    short, pages of the widest request).  Where the last exceeds block_table's width, add nothing to ``taken``: widen the
+    table and call again, or the pages past its columns are lost.
     """
     if _torch is None:
         _load_torch()

@@ -104,3 +104,30 @@ def test_helpers_without_csa_torch_give_the_same(monkeypatch):
     monkeypatch.setattr(serving, "_short", None)
     for s, p in zip(short, calls()):
         assert (s is None and p is None) or torch.equal(s, p)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("held", [0, 2, 3, 5])
+def test_too_narrow_a_table_is_widened_and_the_call_repeated(in_place, held):
+    page, width = 4, 3
+    before, after = i32([held * page, 2, 0]), i32([30, 41, 3])
+    ids = torch.randperm(64, generator=torch.Generator().manual_seed(held)).int().cuda()
+    free, taken = ids[20:].contiguous(), i32([2])
+    narrow = i32([[-1] * width] * 3)
+    narrow[0, :min(held, width)] = ids[:min(held, width)]
+    narrow[1, 0] = ids[9]
+    got, _, _, counts = csa.page_tables(before, after, 1, page, free, narrow, 80, taken=taken, out=narrow if in_place else None)
+    need = counts[3].item()
+    assert need == 11 > width
+    wide = torch.full((3, need), -7, dtype=torch.int32, device="cuda")
+    wide[:, :width] = got
+    # (the caller's own pages past the old width, which the narrow table could not hold)
+    wide[0, width:max(held, width)] = ids[width:max(held, width)]
+    again = csa.page_tables(before, after, 1, page, free, wide, 80, taken=taken)
+    want = u.pages_plain(before.tolist(), after.tolist(), 1, page, free.tolist(),
+                         [ids[:held].tolist() + [-1] * (need - held), [ids[9].item()] + [-1] * (need - 1), [-1] * need], 80, 2)
+    for w, g in zip(want, again):
+        assert list(w) == g.tolist()
+    table = again[0]
+    pages = table[table >= 0]
+    assert pages.unique().numel() == pages.numel() == held + 1 + again[3][1].item()  # each held or taken page in one place
