@@ -40,11 +40,10 @@ template <typename C, int NP> __global__ void __launch_bounds__(kWarps * 32) att
     if (token >= p.n_tokens || token >= __ldg(p.cu_q + p.n_req) || token < __ldg(p.cu_q))
         return;
     const int r = find_segment(p.cu_q, p.n_req, (int)token);
-    const int begin = __ldg(p.cu_q + r), end = __ldg(p.cu_q + r + 1);
+    const int end = __ldg(p.cu_q + r + 1);
     const int64_t held = (int64_t)__ldg(p.seq_lens + r) - (end - token) + 1;
     const int64_t most = (int64_t)p.width * p.page_size;
     const int rows = (int)(held < 0 ? 0 : min(held / p.ratio, most));
-    (void)begin;
     float2 q[NP], o[NP];
     const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(p.q) + token * p.q_token_stride + head * p.q_head_stride;
 #pragma unroll

@@ -235,8 +235,9 @@ template <typename T, typename OUT> cudaError_t fwd_size(const NormFwdParams &p,
         if (words <= 256) return fwd_go<T, OUT, V, 128, 2>(p, st);
         if (words <= 512) return fwd_go<T, OUT, V, 128, 4>(p, st);
         if (words <= 1024) return fwd_go<T, OUT, V, 256, 4>(p, st);
-        if (words <= 2048) return fwd_go<T, OUT, V, 512, 4>(p, st);
-        return fwd_go<T, OUT, V, 1024, 4>(p, st);
+        if constexpr (V == 4)  // (16384 columns of 16 bits are 2048 words)
+            if (words > 2048) return fwd_go<T, OUT, V, 1024, 4>(p, st);
+        return fwd_go<T, OUT, V, 512, 4>(p, st);
     }
     if constexpr (sizeof(T) == 2)
         if (vec == 2) {

@@ -224,8 +224,9 @@ cudaError_t bwd_size(const NormBwdParams &p, int vec, float *partial, int *block
         if (words <= 256) return bwd_go<T, V, 128, 2>(p, partial, blocks, plan, st);
         if (words <= 512) return bwd_go<T, V, 256, 2>(p, partial, blocks, plan, st);
         if (words <= 1024) return bwd_go<T, V, 512, 2>(p, partial, blocks, plan, st);
-        if (words <= 2048) return bwd_go<T, V, 1024, 2>(p, partial, blocks, plan, st);
-        return bwd_go<T, V, 1024, 4>(p, partial, blocks, plan, st);
+        if constexpr (V == 4)  // (16384 columns of 16 bits are 2048 words)
+            if (words > 2048) return bwd_go<T, V, 1024, 4>(p, partial, blocks, plan, st);
+        return bwd_go<T, V, 1024, 2>(p, partial, blocks, plan, st);
     }
     if constexpr (sizeof(T) == 2)
         if (vec == 2) {
