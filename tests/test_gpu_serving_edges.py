@@ -5,6 +5,7 @@ import torch
 
 import serving_util as u
 import sparse_attention_kv_csa_gb300 as csa
+from test_gpu_latent import check, made
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +132,183 @@ def test_too_narrow_a_table_is_widened_and_the_call_repeated(in_place, held):
     table = again[0]
     pages = table[table >= 0]
     assert pages.unique().numel() == pages.numel() == held + 1 + again[3][1].item()  # each held or taken page in one place
+
+
+# ---- the norm's ring of rows: taken where the blocks that the rows need exceed three times the resident ones; these counts
+# exceed three times what 152 SMs of 2048 threads can hold, whatever the registers.
+#
+# Bounds, u = 2^-24, as in test_gpu_norm.py: rstd from a sum of dim squares, (dim / 2 + 8) u; y three roundings more, 8-bit
+# scales at most eight more; out one rounding to its type; the gradient's mean sums dim products.
+U = 2.0 ** -24
+
+
+def rows_of(n, dim, dtype, seed, stride=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((n, dim + stride), device="cuda", generator=g) * torch.exp(0.5 * torch.randn(dim + stride, device="cuda", generator=g))
+    return x.to(dtype)[:, :dim]
+
+
+@pytest.mark.parametrize("n,dim,dtype,residual,group,stride", [
+    (30011, 512, torch.bfloat16, False, 0, 0), (30011, 512, torch.float16, True, None, 8), (30013, 384, torch.float32, True, 128, 4),
+    (40009, 128, torch.bfloat16, True, 128, 64), (30011, 1024, torch.bfloat16, False, 128, 0),
+    (7501, 2048, torch.bfloat16, True, None, 0), (7501, 4096, torch.bfloat16, True, 128, 0), (7501, 4096, torch.float16, False, 0, 24),
+    (3701, 4096, torch.float32, True, 128, 0), (3701, 8192, torch.bfloat16, True, 0, 0), (1901, 16384, torch.bfloat16, True, 128, 8),
+    (1901, 8192, torch.float32, False, None, 0), (1001, 16384, torch.float32, True, None, 0), (1001, 16384, torch.float32, True, 128, 0)])
+def test_ring_forward(n, dim, dtype, residual, group, stride):
+    """group None: output of x's type, else 8 bits."""
+    x, w = rows_of(n, dim, dtype, 31, stride), rows_of(1, dim, torch.float32, 32)[0]
+    r = rows_of(n, dim, dtype, 33, stride) if residual else None
+    kw = {} if group is None else dict(out_dtype=torch.float8_e4m3fn, scale_group=group)
+    out, scales, total, rstd = csa.rms_norm_forward(x, w, 1e-6, residual=r, **kw)
+    h, y, rs = u.norm64(x, w, 1e-6, r)
+    e = (dim / 2 + 16) * U
+    assert total is None if r is None else torch.equal(total, h)
+    assert ((rstd.double() - rs).abs() <= e * rs).all()
+    if group is None:
+        small = 1e-7 if dtype == torch.float16 else 0.0
+        assert ((out.double() - y).abs() <= (u.HALF[dtype] * (1 + e) + 2 * e) * y.abs() + small).all()
+    else:
+        y = y.view(n, -1, group or dim)
+        want = y.abs().amax(2) / 448
+        assert ((scales.double() - want).abs() <= e * want).all()
+        got = out.double().view_as(y) * scales.double()[..., None]
+        assert ((got - y).abs() <= (2.0 ** -4 + 2 * e) * y.abs() + (2.0 ** -10 + 2 * e) * want[..., None]).all()
+    again = csa.rms_norm_forward(x, w, 1e-6, residual=r, **kw)
+    assert torch.equal(again[0].view(torch.uint8), out.view(torch.uint8)) and torch.equal(again[3], rstd)
+
+
+@pytest.mark.parametrize("n,dim,dtype,residual,stride", [
+    (30011, 512, torch.bfloat16, True, 0), (30011, 256, torch.float16, False, 8), (30011, 128, torch.float32, True, 0),
+    (15013, 1024, torch.bfloat16, True, 16), (7501, 2048, torch.bfloat16, False, 0), (7501, 1024, torch.float32, True, 4),
+    (3701, 4096, torch.bfloat16, True, 0), (3701, 4096, torch.float16, False, 40), (1901, 8192, torch.bfloat16, True, 0),
+    (1001, 16384, torch.bfloat16, True, 0), (1001, 8192, torch.float32, True, 0), (1001, 16384, torch.float32, True, 0),
+    (1001, 16384, torch.float32, False, 8)])
+def test_ring_backward(n, dim, dtype, residual, stride):
+    h, w = rows_of(n, dim, dtype, 41, stride), rows_of(1, dim, torch.float32, 42)[0]
+    dy = rows_of(n, dim, dtype, 43, stride)
+    dh = rows_of(n, dim, dtype, 44, stride) if residual else None
+    rstd = h.float().square().mean(1).add(1e-6).rsqrt()
+    dx, dw = csa.rms_norm_backward(dy, h, w, rstd, grad_residual=dh)
+    gd, unit = dy.double(), h.double() * rstd.double()[:, None]
+    wg, rd = w.double() * gd, rstd.double()[:, None]
+    want = rd * (wg - unit * (wg * unit).mean(1, keepdim=True))
+    tol = 8 * U * rd * (wg.abs() + unit.abs() * (wg * unit).abs().mean(1, keepdim=True) * (dim + 8) / 4)
+    if residual:
+        want = want + dh.double()
+        tol = tol + 2 * U * dh.double().abs()
+    tol = tol + u.HALF[dtype] * (want.abs() + tol) + (1e-7 if dtype == torch.float16 else 0.0)
+    assert ((dx.double() - want).abs() <= tol).all()
+    terms = gd * unit
+    assert ((dw.double() - terms.sum(0)).abs() <= (n + 8) * U * terms.abs().sum(0)).all()
+    again = csa.rms_norm_backward(dy, h, w, rstd, grad_residual=dh)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+IN_PLACE = [(1, 8, torch.bfloat16), (300, 1001, torch.bfloat16), (300, 1002, torch.float16), (33001, 128, torch.bfloat16),
+            (30011, 512, torch.bfloat16), (7501, 4096, torch.bfloat16), (3701, 4096, torch.float32), (9, 16384, torch.float32),
+            (1001, 16384, torch.float32), (40000, 333, torch.float32)]
+CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@pytest.mark.parametrize("n,dim,dtype", IN_PLACE)
+def test_forward_in_place(n, dim, dtype):
+    x, r, w = rows_of(n, dim, dtype, 51).contiguous(), rows_of(n, dim, dtype, 52).contiguous(), rows_of(1, dim, torch.float32, 53)[0]
+    want = csa.rms_norm_forward(x, w, 1e-6, residual=r)
+    alone = csa.rms_norm_forward(x, w, 1e-6)
+    a = x.clone()
+    assert torch.equal(csa.rms_norm_forward(a, w, 1e-6, out=a)[0], alone[0])
+    for out_is_x in (True, False):
+        a, b, rstd = x.clone(), r.clone(), torch.empty(n, device="cuda")
+        out, total = (a, b) if out_is_x else (b, a)
+        csa.csa_rms_norm_fwd(a, dim, b, dim, w, n, dim, 1e-6, CODES[dtype], None, 0, out, dim, CODES[dtype], None, 0, total, rstd)
+        assert torch.equal(out, want[0]) and torch.equal(total, want[2]) and torch.equal(rstd, want[3])
+
+
+@pytest.mark.parametrize("n,dim,dtype", IN_PLACE)
+def test_backward_in_place(n, dim, dtype):
+    h, dy, dh = (rows_of(n, dim, dtype, s).contiguous() for s in (54, 55, 56))
+    w = rows_of(1, dim, torch.float32, 57)[0]
+    rstd = h.float().square().mean(1).add(1e-6).rsqrt()
+    want = csa.rms_norm_backward(dy, h, w, rstd, grad_residual=dh)
+    for onto_dy in (True, False):
+        a, b, dw = dy.clone(), dh.clone(), torch.empty(dim, device="cuda")
+        dx = a if onto_dy else b
+        csa.csa_rms_norm_bwd(h, dim, a, dim, b, dim, w, rstd, n, dim, CODES[dtype], dx, dw)
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("first,dim", [(0, 512), (8, 512), (1, 512), (3, 333), (2, 334)])
+def test_strided_output_holds_the_norm(dtype, first, dim):
+    big = rows_of(20, 1100, dtype, 61)
+    x, r = big[2:17, first:first + dim], big[1:16, first + 64:first + 64 + dim]
+    for base in (0, 1, 8):
+        room = torch.full((15, dim + 24), 7.0, dtype=dtype, device="cuda")
+        csa.rms_norm_forward(x, None, residual=r, out=room[:, base:base + dim])
+        _, y, _ = u.norm64(x, None, 1e-6, r)
+        e, small = (dim / 2 + 16) * U, 1e-7 if dtype == torch.float16 else 0.0
+        assert ((room[:, base:base + dim].double() - y).abs() <= (u.HALF[dtype] + 2 * e) * y.abs() + small).all()
+        assert (room[:, :base] == 7).all() and (room[:, base + dim:] == 7).all()
+
+
+# ---- attention: what only wide rows in odd pages, many requests, long requests among short ones, or large totals reach
+
+
+@pytest.mark.parametrize("dim,v_dim", [(256, 256), (320, 320), (512, 512), (576, 512)])
+@pytest.mark.parametrize("page", [1, 3, 50])
+@pytest.mark.parametrize("bits8", [False, True])
+def test_wide_rows_in_odd_pages(dim, v_dim, page, bits8):
+    check(made([513, 64, 200, 3], [1, 1, 9, 3], 16, dim, 1, page, bits8, True, seed=dim + page), v_dim)
+
+
+@pytest.mark.parametrize("dim,bits8", [(64, False), (128, True), (512, False), (200, False)])
+def test_more_requests_than_the_division_keeps(dim, bits8):
+    lens = [(7 * i) % 90 for i in range(3000)]
+    check(made(lens, [min(1, a) for a in lens], 4, dim, 2, 16, bits8, seed=60))
+
+
+@pytest.mark.parametrize("dim,page,bits8", [(512, 64, False), (512, 64, True), (128, 64, False), (576, 16, False), (256, 50, False)])
+@pytest.mark.parametrize("where", [0, 9, 19])
+def test_a_long_request_among_short_ones(dim, page, bits8, where):
+    lens = [40 + i for i in range(20)]
+    lens[where] = 12001
+    check(made(lens, [1] * 20, 16, dim, 1, page, bits8, True, seed=61), min(dim, 512))
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("lens,news,ratio", [([900], [300], 4), ([5000, 131], [260, 130], 128)])
+def test_prompts(lens, news, ratio, bits8):
+    check(made(lens, news, 64, 512, ratio, 64, bits8, True, seed=62))
+
+
+def test_units_past_2_to_the_20():
+    # 5000 tokens of 64 heads, an item each, over 11384 to 16384 rows in tiles of 64: more than 5000 * (177 + 3) on average 220
+    new, total, heads, dim, page = 5000, 16384, 64, 64, 64
+    assert sum((total - new + i + 1 + 63) // 64 + 3 for i in range(new)) >= 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(63)
+    cache = torch.randn((total // page, page, dim), device="cuda", generator=g).bfloat16()
+    table = torch.randperm(total // page, device="cuda", generator=g).int()[None]
+    q = torch.randn((new, heads, dim), device="cuda", generator=g).bfloat16()
+    out, lse = csa.latent_attention(q, cache, table, i32([0, new]), i32([total]), 1, 0.125)
+    torch.cuda.synchronize()
+    for t in sorted({0, 1, new - 1, *range(17, new, 61)}):
+        a = dict(q=q[t:t + 1], cache=cache, block_table=table, cu_q=i32([0, 1]), seq_lens=i32([total - new + t + 1]), ratio=1, scale=0.125)
+        check(a, out=out[t:t + 1], lse=lse[t:t + 1])
+
+
+@pytest.mark.parametrize("dim,bits8", [(512, False), (512, True), (128, False), (96, False), (96, True)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("row", [100, 128])
+def test_every_query_that_sees_a_bad_row_shows_it(dim, bits8, bad, row):
+    # of 130 rows the last four belong to the new tokens: token i sees rows up to 126 + i, so row 128 is seen by two of them
+    a = made([130], [4], 8, dim, 1, 64, bits8, seed=8)
+    out, lse = check(a)
+    at = (a["block_table"][0, row // 64], row % 64)
+    if bits8:
+        a["row_scales"][at] = bad
+    else:
+        a["cache"][at][5] = bad
+    sees = max(0, row - 126)
+    out2, lse2 = csa.latent_attention(**a)
+    assert torch.equal(out[:sees], out2[:sees]) and torch.equal(lse[:sees], lse2[:sees])
+    assert not out2[sees:].isfinite().all(2).any()
