@@ -56,12 +56,6 @@ constexpr int kQueryWarps = 4;                    // rows by TMA: warps that bri
 template <Rows ROWS, int NK>
 constexpr int kThreadsOf = 32 * (ROWS == kTma ? kTmaWarp + 1 + kQueryWarps : kMmaWarp + 1 + load_warps(ROWS, NK));
 constexpr int kMaxStages = 4;
-// Units of an item besides its tiles, for its queries and output: a decode step of 64 requests 83.8, 81.2 and 80.2 us with
-// 1, 2 and 3, of 129 requests with 8-bit rows 150.2, 148.0 and 145.4.
-constexpr int kHead = 3;
-// Units of a block's share at least.  Eight requests of 1024 rows: 26.1, 23.5 and 22.2 us with 4, 3 and 2; one of 16384
-// rows: 26.9, 27.6 and 32.0.
-constexpr int kMinUnits = 3;
 constexpr int kKept = 2048;                       // requests whose facts are kept in shared memory while work is cut
 constexpr int kScores = 4;                        // S tiles in tensor memory
 constexpr float kLog2E = 1.44269504088896340736f;
@@ -152,14 +146,13 @@ template <int R> struct Walk {
                 q = request(p, r);
             }
             nt = item_tiles<R>(p, q, m);
-            const int take = (int)min((long long)(nt + kHead - off), left);
-            const bool head = off == 0;
-            t0 = max(off - kHead, 0);
-            t1 = max(off + take - kHead, 0);
-            left -= take;
+            const Segment s = segment_of(nt, off, left);
+            t0 = s.t0;
+            t1 = s.t1;
+            left -= s.take;
             off = 0;
             ++m;
-            if (t1 > t0 || (nt == 0 && head))
+            if (s.some)
                 return true;
         }
         return false;
@@ -193,24 +186,6 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
 {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
     return f2_to_bf16x2(__half22float2(*reinterpret_cast<const __half2 *>(&h)));
-}
-
-// Unit cut: block c's first unit.
-__device__ __forceinline__ long long cut(long long total, int c, int g)
-{
-    return total < (1 << 20) ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)g) : total * c / g;  // c < 4096
-}
-
-// The block whose share holds a unit.
-__device__ __forceinline__ int holder(long long unit, long long total, int g)
-{
-    return total < (1 << 20) ? (int)(((uint32_t)(unit + 1) * (uint32_t)g - 1) / (uint32_t)total) : (int)(((unit + 1) * g - 1) / total);
-}
-
-// How many blocks share the units.
-__device__ __forceinline__ int sharing(long long total, int blocks)
-{
-    return (int)max(1ll, min(total / kMinUnits, (long long)blocks));
 }
 
 template <Rows ROWS, int NK, int R>

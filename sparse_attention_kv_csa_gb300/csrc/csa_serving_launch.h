@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "csa_latent_cuts.h"
 #include "csa_serving.h"
 
 namespace csa {
@@ -61,23 +62,6 @@ struct PageParams {
 };
 constexpr int kMaxRequests = 14000;  // two prefix sums of this length fit an SM's shared memory
 cudaError_t launch_page_tables(const PageParams &p, int num_sms, cudaStream_t st);
-
-// n / d for 0 <= n < 2^31 by a multiplication (T. Granlund and P. Montgomery, "Division by invariant integers using
-// multiplication", PLDI 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (hi(m n) + n) >> l.
-struct Divider {
-    uint32_t m, l, d;
-    Divider() = default;
-    explicit Divider(uint32_t divisor) : m(0), l(0), d(divisor)
-    {
-        while (l < 31 && (1u << l) < d)
-            ++l;
-        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> l; }
-    __device__ __forceinline__ uint32_t remainder(uint32_t n) const { return n - quotient(n) * d; }
-#endif
-};
 
 struct AttnParams {
     const void *q;

@@ -26,3 +26,16 @@ def pytest_collection_modifyitems(config, items):
     for it in items:
         if "gpu" in it.keywords:
             it.add_marker(skip)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def status_word(request):
+    """Every module that ran on the GPU leaves the device's status word clear (no bounded wait gave up)."""
+    yield
+    if "torch" not in sys.modules:
+        return
+    import torch
+    if torch.cuda.is_available() and torch.cuda.is_initialized():
+        import sparse_attention_kv_csa_gb300 as csa
+        torch.cuda.synchronize()
+        assert csa.csa_device_status() == 0, csa.csa_last_error_message()
