@@ -33,14 +33,16 @@ typedef enum csa_dtype {
  *   h = round(x + residual)    rounded to dtype (h = x when residual is NULL)
  *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight      in fp32
  *   out = round(y) in dtype, or with out_dtype E4M3: scale = max|y| / 448 over scale_group columns (0: the whole row;
- *   128), out = e4m3(y / scale); a group of zeros has scale 0.
+ *   128), out = e4m3(y / scale); a group of zeros has scale 0, one with a NaN among its y scale NaN.
+ *   y / scale is y times the rounded reciprocal: a quotient within two fp32 roundings of the middle between two 8-bit values
+ *   may go to the other one.
  *
  * x, residual: [n_rows, dim] of dtype (BF16, F16 or F32), row strides in elements, at least dim.  weight: fp32 [dim]
  * or NULL (ones).  out_dtype: dtype or E4M3.  slots: int64 [n_rows] or NULL; row i goes to row slots[i] of out and
  * scales, and nowhere when slots[i] is outside [0, n_slots) (distinct rows need distinct slots); without slots row i
  * goes to row i and n_slots is ignored.  scales: fp32 [rows of out, groups], E4M3 only.  residual_out (h, contiguous) and rstd (fp32
- * [n_rows]) may be NULL.  Without slots out and residual_out may be x or residual themselves (same stride); otherwise
- * outputs overlap no input.
+ * [n_rows]) may be NULL.  Without slots an out of dtype and residual_out may be x or residual themselves (same stride);
+ * otherwise outputs overlap no input.
  * dim in [1, 16384]; scale_group 128 needs dim a multiple of 128 and 16-byte aligned bases and strides
  * (CSA_ERR_MISALIGNED); everything else takes any alignment of its elements, faster where rows are 16-byte aligned.
  */
@@ -74,11 +76,13 @@ CSA_API int csa_rms_norm_bwd(const void *h, int64_t h_stride, const void *grad_o
  *   counts    [4]             new rows, pages taken, pages short, the most pages that a request needs
  * taken: device int32 or NULL, the entries of free_pages [n_free] that are already used.  table: [n_req, width] with
  * row stride table_stride; table_out is contiguous and may be table itself when table_stride == width.  All arrays
- * are int32 unless said otherwise.  A table narrower than a need (counts[3] > width) holds none of the pages past its
- * columns, although counts[1] counts them and later requests get the entries of free_pages behind them: such a result is
- * not to be kept.  Call again with a table of counts[3] columns or more (those past the pages that a request holds may
- * have anything in them) and the same taken, which gives what the wider table would have given at once, after a call in place too.  Negative lengths count as 0.  n_req <= 14000.  Sums of rows and of pages are held at
+ * are int32 unless said otherwise.  Negative lengths count as 0.  n_req <= 14000.  Sums of rows and of pages are held at
  * 2^31 - 1.
+ *
+ * A table narrower than a need (counts[3] > width) holds none of the pages past its columns, although counts[1] counts
+ * them and later requests get the entries of free_pages behind them: such a result is not to be kept.  Call again with a
+ * table of counts[3] columns or more (those past the pages that a request holds may have anything in them) and the same
+ * taken, which gives what the wider table would have given at once, after a call in place too.
  */
 CSA_API int csa_page_tables(const int32_t *before, const int32_t *after, int32_t n_req, int32_t ratio, int32_t page_size,
                     const int32_t *free_pages, int32_t n_free, const int32_t *taken, const int32_t *table,
@@ -100,7 +104,7 @@ CSA_API int csa_page_tables(const int32_t *before, const int32_t *after, int32_t
  * cache      [n_pages, page_size, head_dim], row stride cache_stride in elements; BF16, or E4M3 with
  * row_scales fp32 [n_pages * page_size]: a row's values are e4m3 * scale
  * block_table int32 [n_req, width], row stride table_stride; an entry outside [0, n_pages) hides its rows
- * sink       fp32 [n_heads] or NULL
+ * sink       fp32 [n_heads], finite or -inf, or NULL
  * out        bf16 [n_tokens, n_heads, v_dim] contiguous;  lse fp32 [n_tokens, n_heads] or NULL
  *
  * n_req <= 14000, n_heads <= 4096, n_tokens * n_heads < 2^31; n_pages * page_size and width * page_size at most

@@ -14,6 +14,12 @@ same CUDA device.  Gradients flow to kv, score and ape; the offsets and the
 static capacity are not differentiable.  The backward rebuilds the softmax from
 kv / score / ape (nothing but the inputs is saved), so the saved tensors must not
 be modified in place between the two passes (autograd's version counter checks).
+
+``rms_norm(x, weight, residual, eps)`` is the norm of include/csa_serving.h in the same manner; it saves x (+ residual)
+and the rows' reciprocal roots.
+
+A forward and backward captured into a CUDA graph want leaves of their own (x.detach().clone().requires_grad_()): while
+an eager graph of the same leaves lives, torch may end the process in the captured backward.
 """
 import torch
 

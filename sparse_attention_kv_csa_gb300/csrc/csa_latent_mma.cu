@@ -46,9 +46,11 @@ constexpr int kGroupChunk = 8 * 128;              // bytes of 64 columns of eigh
 constexpr int kSoftWarps = 4;
 constexpr int kMmaWarp = 4;
 // Blocks an SM: two where the shared memory and tensor memory of each allow it (rows of up to 256 columns), whose waits
-// then overlap: 1024 tokens over 4096 rows of 128 columns 151 us with one, 109 with two, a decode step of 64 requests 31.6
-// and 27.5.  Rows through registers are brought by eight warps or, to leave registers for two blocks, four; for their
-// 256 columns one block is better (8-bit decode step 39.5 us, with two 40.9).
+// then overlap (64 heads: 1024 tokens over 4096 rows of 128 columns 377 us with one, 240 with two, a decode step of 64 requests
+// of up to 8192 rows 42.4 and 36.3; of 256 columns 383 and 332, but the decode step 46.6 and 52.5).  Rows through registers
+// are brought by eight warps or, to leave registers for two blocks, four, which then spill some 250 bytes a thread (decode
+// steps of 64 and 128 8-bit columns 48.7 and 53.3 us with one block, 42.9 and 49.3 with two); for their 256 columns one
+// block is better (55.7 and 63.1 us, in pages of 50 bf16 rows 66 and 75).
 constexpr int per_sm(Rows how, int nk) { return nk <= (how == kTma ? 4 : 3) ? 2 : 1; }
 constexpr int load_warps(Rows how, int nk) { return 8 / per_sm(how, nk); }
 constexpr int kTmaWarp = 5;                       // rows by TMA

@@ -218,7 +218,7 @@ template <typename T, typename OUT> cudaError_t fwd_size(const NormFwdParams &p,
     if (vec == V) {
         const int words = p.dim / V;
         // Many narrow rows: two a warp, which halves what a row costs besides its elements (200000 rows of 128 46 us with
-        // one, 29 with two; 131288 of 512 to 8 bits 66 and 63); few: one, which is done sooner (8256 of 512 6.5 and 7.7).
+        // one, 29 with two; 131288 of 512 to 8 bits 66 and 64); few: one, which is done sooner (8256 of 512 6.5 and 7.7).
         // Types of 16 bits alone: half a warp's words have to hold a group of 128 columns.
         if constexpr (V == 8) {
             if (words <= 64 && p.n_rows >= 32768) {
@@ -229,7 +229,7 @@ template <typename T, typename OUT> cudaError_t fwd_size(const NormFwdParams &p,
         }
         if (words <= 32) return fwd_go<T, OUT, V, 32, 1>(p, st);
         if (words <= 64) return fwd_go<T, OUT, V, 32, 2>(p, st);
-        // (200000 rows of 576 to 8 bits: 170 us with four words a thread, 149 with three)
+        // (200000 rows of 576 to 8 bits: 170 us with four words a thread, 152 with three)
         if (words <= 96) return fwd_go<T, OUT, V, 32, 3>(p, st);
         if (words <= 128) return fwd_go<T, OUT, V, 32, 4>(p, st);
         if (words <= 256) return fwd_go<T, OUT, V, 128, 2>(p, st);

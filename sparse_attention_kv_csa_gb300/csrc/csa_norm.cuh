@@ -13,10 +13,10 @@
 //
 // Both are bound by DRAM: every array is read or written once and a row stays in registers between its sums and its
 // output.  A row belongs to one team of 16 to 1024 threads; a block holds one team (or several small ones) and walks
-// the rows with the grid's stride, its weights in registers.  Rows of 16-byte vectors for teams of 128 threads or more
-// come by bulk copies into a ring of rows in shared memory, several rows ahead (loads into registers a row ahead kept
-// too few bytes on the way: 130 against 95 us for 16411 rows of 4096 with 8-bit output); other rows are loaded into
-// registers a row ahead.  All sums are fp32; h is rounded to T before the norm because that is what the next layer and
+// the rows with the grid's stride, its weights in registers.  Rows of whole 16-byte vectors, where there are more than three
+// a resident team, come by bulk copies into a ring of rows in shared memory, several rows ahead (loads into registers a row
+// ahead kept too few bytes on the way: 130 against 95 us for 16411 rows of 4096 with 8-bit output); other rows are loaded
+// into registers a row ahead.  All sums are fp32; h is rounded to T before the norm because that is what the next layer and
 // the backward read.  dw: one partial row per block, added in a fixed order by a second kernel (no atomics).
 #pragma once
 

@@ -8,7 +8,7 @@
 //
 // Bound by launch latency for a decode step (a few hundred KB at most) and by the table's bytes for large batches.
 // One launch: the prefix sums run over two integers a request, so every block forms all of them in shared memory
-// (16384 requests are 128 KB) instead of waiting for another kernel, then takes its share of the table and slots.
+// (14000 requests are 112 KB) instead of waiting for another kernel, then takes its share of the table and slots.
 #include "csa_device.cuh"
 #include "csa_launch.h"
 #include "csa_serving_launch.h"

@@ -2,9 +2,11 @@
 
 Argument checks and marshalling for the entry points of include/csa_serving.h; the arithmetic runs in the CUDA kernels
 of libcsa.so.  Ordinary calls (contiguous tensors, the current stream) go through csa_torch, which checks, allocates and
-calls in C++; everything else, and every refusal, through the checks here.  The helpers allocate their outputs with torch and launch on ``stream`` (a torch.cuda.Stream, a raw
-cudaStream_t integer, or None for torch's current stream); no call synchronises.  Tensors live on the current CUDA
-device; ValueError / TypeError name an argument that does not fit, CSAError a call that the library refuses.
+calls in C++; everything else, and every refusal, through the checks here, as does every call where csa_torch cannot be
+built or loaded.  The helpers allocate their outputs with torch and launch on ``stream`` (a torch.cuda.Stream, a raw
+cudaStream_t integer, or None for torch's current stream); no call synchronises, and inputs handed to another stream than
+their own have to live until it has read them.  Tensors live on the current CUDA device; ValueError / TypeError name an
+argument that does not fit, CSAError a call that the library refuses.
 
     out, scales, stream, rstd = rms_norm_forward(x, weight, eps, residual=..., out_dtype=..., slots=...)
     grad_x, grad_weight       = rms_norm_backward(grad_out, h, weight, rstd, grad_residual=...)
@@ -362,6 +364,8 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
     cache [n_pages, page_size, head_dim], bf16, or float8_e4m3fn with row_scales fp32 [n_pages, page_size]; block_table
     int32 [n_req, width]; cu_q int32 [n_req + 1]; seq_lens int32 [n_req], tokens of each request with the new ones;
     ratio: tokens a row; v_dim: leading columns that are the values (all by default); sink fp32 [n_heads] or None.
+    Multiples of 64 up to 576 columns with a v_dim of up to 512 run on the tensor cores, other widths (576 columns with
+    the default v_dim among them) on the fp32 units, more than a hundred times slower.  Tokens outside of cu_q are left unwritten.
     Returns (out bf16 [n_tokens, n_heads, v_dim], lse fp32 [n_tokens, n_heads]); see csa_latent_attention.
     """
     if _torch is None:
