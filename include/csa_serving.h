@@ -1,7 +1,8 @@
 /*
- * csa_serving.h -- the operators of libcsa around serving the Compressor's rows: the norm that writes rows (in 8 bits
- * with scales, to the slots of a paged cache), the tables that say where a request's rows lie, and the attention
- * whose keys and values are those rows.
+ * csa_serving.h -- the operators of libcsa around serving the Compressor's rows: the norms, one of which writes rows (in
+ * 8 bits with scales) to the slots of a paged cache, the append of rows to such a cache with the position rotation on the
+ * way, the tables that say where a request's rows lie, and the attention whose keys and values are those rows, for
+ * requests by themselves and for a batch that shares a prefix.
  *
  * The conventions are csa.h's: device pointers on the current device, caller-owned; every call is asynchronous on
  * `stream`, never synchronises, and returns a csa_status (csa_last_error_message() has the text); a failed validation
@@ -66,6 +67,69 @@ CSA_API int csa_rms_norm_bwd(const void *h, int64_t h_stride, const void *grad_o
                      float *grad_weight, void *stream);
 
 /*
+ * Layer norm with the residual's addition:
+ *   h = round(x + residual)    rounded to dtype (h = x when residual is NULL)
+ *   mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps),  out = round((h - mean) * rstd * weight + bias)   in fp32
+ *
+ * x, residual: [n_rows, dim] of dtype (BF16, F16 or F32), row strides in elements, at least dim.  weight, bias: fp32 [dim]
+ * or NULL (ones, zeros).  residual_out (h, contiguous), mean and rstd (fp32 [n_rows]) may be NULL.  out and residual_out may
+ * be x or residual themselves (same stride); otherwise outputs overlap no input.  dim in [1, 16384]; any alignment of the
+ * elements, faster where rows are 16-byte aligned.
+ */
+CSA_API int csa_layer_norm_fwd(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                       const float *weight, const float *bias, int64_t n_rows, int32_t dim, float eps, int32_t dtype,
+                       void *out, int64_t out_stride, void *residual_out, float *mean, float *rstd, void *stream);
+
+/*
+ * Gradient of csa_layer_norm_fwd, from h (residual_out, or x without a residual), mean and rstd, with
+ * u = (h - mean) * rstd and g = weight * grad_out:
+ *   grad_x = rstd * (g - mean_of(g) - u * mean_of(g * u)) + grad_residual     (the residual's gradient is the same)
+ *   grad_weight = sum over rows of grad_out * u,  grad_bias = sum over rows of grad_out   (fp32, fixed order; overwritten)
+ * grad_residual: the gradient that reaches residual_out, or NULL.  grad_x is contiguous [n_rows, dim] and may be
+ * grad_out or grad_residual itself when that is contiguous.  weight NULL: ones; grad_weight and grad_bias may be NULL.
+ * n_rows == 0 writes zeros to them.
+ */
+CSA_API int csa_layer_norm_bwd(const void *h, int64_t h_stride, const void *grad_out, int64_t grad_out_stride,
+                       const void *grad_residual, int64_t grad_residual_stride, const float *weight, const float *mean,
+                       const float *rstd, int64_t n_rows, int32_t dim, int32_t dtype, void *grad_x, float *grad_weight,
+                       float *grad_bias, void *stream);
+
+/*
+ * Rows appended to a paged cache, their last rot_dim columns rotated by the row's position, and queries rotated beside them.
+ * A row is rows[i] with the rotated columns last, or, with rotary, rows[i] (row_dim columns) followed by the rotation of
+ * rotary[i] (rot_dim columns); width = row_dim, or row_dim + rot_dim.  The columns to rotate are rot_dim / 2 pairs (a, b),
+ * pair i columns (2 i, 2 i + 1) when interleaved, else (i, i + rot_dim / 2):
+ *   (a, b) -> (a cos - b sin, a sin + b cos)      in fp32, one rounding
+ * with cos = rotation[position][i] and sin = rotation[position][rot_dim / 2 + i].
+ *
+ * rows, rotary, q: dtype (BF16, F16 or F32); row strides in elements.  positions: int32 [n_rows]; a position outside
+ * [0, n_positions) makes the rotated columns NaN.  rotation: fp32 [n_positions, rot_dim], contiguous.  slots: int64 [n_rows];
+ * row i goes to row slots[i] of out and nowhere when that is outside [0, n_slots) (distinct rows need distinct slots).
+ * out: [n_slots, width], dtype or E4M3; with E4M3 scales fp32 [n_slots] gets max|row| / 448 and out e4m3(row / scale) (a row of
+ * zeros has scale 0, one with a NaN scale NaN; the quotient as in csa_rms_norm_fwd).
+ * q: n_tokens tokens of n_heads heads, rot_dim columns each, element (token, head, c) at token * q_token_stride +
+ * head * q_head_stride + c; rotated to q_out (strides of its own; q itself when the strides agree) by q_positions int32
+ * [n_tokens].  n_rows 0 or n_tokens 0: nothing of that kind is done.  Otherwise outputs overlap no input.
+ * rot_dim even in [2, 1024], width at most 1024, n_tokens * n_heads < 2^31.  Any alignment of the elements; faster where rows
+ * are 16-byte aligned and halves (interleaved: parts) are whole 16-byte vectors.
+ */
+CSA_API int csa_append_rows(const void *rows, int64_t row_stride, int32_t row_dim, const void *rotary, int64_t rotary_stride,
+                    int32_t rot_dim, const int32_t *positions, int64_t n_rows, int32_t dtype, const float *rotation,
+                    int64_t n_positions, int32_t interleaved, const int64_t *slots, int64_t n_slots, void *out,
+                    int64_t out_stride, int32_t out_dtype, float *scales, const void *q, int64_t q_token_stride,
+                    int64_t q_head_stride, const int32_t *q_positions, int64_t n_tokens, int32_t n_heads, void *q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, void *stream);
+
+/*
+ * The rotation of csa_append_rows alone, over n_heads heads of n_tokens tokens, or with inverse its inverse (by the negated
+ * angle): what an attention's output takes whose values were rotated with the keys, and the rotation's gradient.  out may be
+ * x itself when the strides agree.
+ */
+CSA_API int csa_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions, int64_t n_tokens,
+               int32_t n_heads, int32_t rot_dim, int32_t dtype, const float *rotation, int64_t n_positions, int32_t interleaved,
+               int32_t inverse, void *out, int64_t out_token_stride, int64_t out_head_stride, void *stream);
+
+/*
  * Block tables, offsets and slots of a paged cache of compressed rows.  Request r goes from before[r] to after[r]
  * tokens, that is from floor(before/ratio) to floor(after/ratio) rows (never fewer than before), in pages of
  * page_size rows:
@@ -121,6 +185,25 @@ CSA_API int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t 
                          int64_t n_pages, int32_t page_size, const int32_t *block_table, int64_t table_stride,
                          int32_t width, const int32_t *seq_lens, int32_t ratio, float scale, const float *sink,
                          void *out, float *lse, void *stream);
+
+/*
+ * csa_latent_attention for a batch whose requests share prefixes: requests [cu_groups[g], cu_groups[g+1]) have their first
+ * shared_rows[g] rows in common (a system prompt, a document), which are read once for the group instead of once for each
+ * request.  The result is csa_latent_attention's of the same arguments.  block_table lists each request's pages from its first
+ * row on, as there: for the shared rows the same pages, or pages with equal contents (the rows of any one of them may be
+ * the ones that are read).
+ *
+ * cu_groups int32 [n_groups + 1], not decreasing, within [0, n_req]; requests outside of all groups share nothing.
+ * shared_rows int32 [n_groups].  Rows that some token of the group does not see are not shared, whatever shared_rows says.
+ * Everything else, and every limit, as in csa_latent_attention; n_groups <= 14000.
+ */
+CSA_API int csa_shared_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q,
+                         int32_t n_req, int64_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t v_dim,
+                         const void *cache, int64_t cache_stride, int32_t cache_dtype, const float *row_scales,
+                         int64_t n_pages, int32_t page_size, const int32_t *block_table, int64_t table_stride,
+                         int32_t width, const int32_t *seq_lens, const int32_t *cu_groups, const int32_t *shared_rows,
+                         int32_t n_groups, int32_t ratio, float scale, const float *sink, void *out, float *lse,
+                         void *stream);
 
 #ifdef __cplusplus
 }

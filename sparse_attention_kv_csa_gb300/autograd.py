@@ -1,4 +1,4 @@
-"""Training-side wrappers: the Compressor and the root-mean-square norm as ``torch.autograd.Function``s.
+"""Training-side wrappers: the Compressor, the norms and the rotation as ``torch.autograd.Function``s.
 
 ``compress(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, capacity)``
 returns ``out`` ([capacity, head_dim] bf16) and, when autograd asks for it,
@@ -16,16 +16,20 @@ kv / score / ape (nothing but the inputs is saved), so the saved tensors must no
 be modified in place between the two passes (autograd's version counter checks).
 
 ``rms_norm(x, weight, residual, eps)`` is the norm of include/csa_serving.h in the same manner; it saves x (+ residual)
-and the rows' reciprocal roots.
+and the rows' reciprocal roots.  ``layer_norm(x, weight, bias, residual, eps)`` is the layer norm, which saves the rows' means
+too, and ``rotate(x, positions, rotation, interleaved, inverse)`` the position rotation, whose gradient is its inverse.
 
 A forward and backward captured into a CUDA graph want leaves of their own (x.detach().clone().requires_grad_()): while
 an eager graph of the same leaves lives, torch may end the process in the captured backward.
 """
 import torch
 
-from . import csa_compress_bwd, csa_compress_fwd, rms_norm_backward, rms_norm_forward
+from . import (csa_compress_bwd, csa_compress_fwd, layer_norm_backward, layer_norm_forward, rms_norm_backward,
+               rms_norm_forward)
+from . import rotate as _rotate
 
-__all__ = ["CompressFunction", "compress", "RMSNormFunction", "rms_norm"]
+__all__ = ["CompressFunction", "compress", "RMSNormFunction", "rms_norm", "LayerNormFunction", "layer_norm", "RotateFunction",
+           "rotate"]
 
 
 def _check_inputs(kv, score, ape, cu_seqlens, cu_seqlens_comp, ratio, coff, require_cuda=True):
@@ -119,3 +123,62 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6):
     flat = lambda t: None if t is None else t.reshape(-1, shape[-1])  # noqa: E731
     out, total = RMSNormFunction.apply(flat(x), weight, flat(residual), eps)
     return out.view(shape) if residual is None else (out.view(shape), total.view(shape))
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """(out, h) = layer norm of h = x + residual; backward through csa_layer_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        out, total, mean, rstd = layer_norm_forward(x, weight, bias, eps, residual=residual)
+        ctx.save_for_backward(x if total is None else total, weight, mean, rstd)
+        ctx.set_materialize_grads(False)
+        ctx.has_residual, ctx.has_bias = residual is not None, bias is not None
+        return out, total
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out, grad_total):
+        h, weight, mean, rstd = ctx.saved_tensors
+        if grad_out is None:  # only the sum was used
+            return grad_total, None, None, grad_total if ctx.has_residual else None, None
+        grad_x, grad_weight, grad_bias = layer_norm_backward(grad_out.contiguous(), h, weight, mean, rstd,
+                                                             grad_residual=None if grad_total is None else grad_total.contiguous())
+        return (grad_x, None if weight is None else grad_weight, grad_bias if ctx.has_bias else None,
+                grad_x if ctx.has_residual else None, None)
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5):
+    """Differentiable layer norm over the last dimension of x (bf16, f16 or f32; weight and bias fp32 or None).
+
+    Returns the norm of x, or with a residual (norm of x + residual, x + residual): the second is the residual stream,
+    through which gradients flow too.
+    """
+    shape = x.shape
+    flat = lambda t: None if t is None else t.reshape(-1, shape[-1])  # noqa: E731
+    out, total = LayerNormFunction.apply(flat(x), weight, bias, flat(residual), eps)
+    return out.view(shape) if residual is None else (out.view(shape), total.view(shape))
+
+
+class RotateFunction(torch.autograd.Function):
+    """The rotation of csa_rotate; its gradient is the inverse rotation of the gradient."""
+
+    @staticmethod
+    def forward(ctx, x, positions, rotation, interleaved, inverse):
+        ctx.save_for_backward(positions, rotation)
+        ctx.form = interleaved, inverse
+        return _rotate(x, positions, rotation, interleaved=interleaved, inverse=inverse)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        positions, rotation = ctx.saved_tensors
+        interleaved, inverse = ctx.form
+        # (an expanded gradient's strides are not a head's)
+        return _rotate(grad_out.contiguous(), positions, rotation, interleaved=interleaved, inverse=not inverse), None, None, None, None
+
+
+def rotate(x, positions, rotation, interleaved=False, inverse=False):
+    """Differentiable position rotation of x [n_tokens, n_heads, rot_dim] (see serving.rotate); positions and the table have
+    no gradient."""
+    return RotateFunction.apply(x, positions, rotation, interleaved, inverse)

@@ -47,6 +47,69 @@ struct NormBwdParams {
 cudaError_t norm_bwd_blocks(const NormBwdParams &p, int *blocks);
 cudaError_t launch_norm_bwd(const NormBwdParams &p, float *partial, cudaStream_t st);
 
+struct LayerFwdParams {
+    const void *x, *residual;
+    int64_t x_stride, residual_stride;
+    const float *weight, *bias;
+    int64_t n_rows;
+    int dim;
+    float eps;
+    int dtype;
+    void *out;
+    int64_t out_stride;
+    void *residual_out;
+    float *mean, *rstd;
+    unsigned *status;
+    int stages;  // (set by the launcher) rows in a block's ring
+};
+cudaError_t launch_layer_fwd(const LayerFwdParams &p, cudaStream_t st);
+
+struct LayerBwdParams {
+    const void *h, *grad_out, *grad_residual;
+    int64_t h_stride, grad_out_stride, grad_residual_stride;
+    const float *weight, *mean, *rstd;
+    int64_t n_rows;
+    int dim, dtype;
+    void *grad_x;
+    float *grad_weight, *grad_bias;
+    unsigned *status;
+    int stages;  // (set by the launcher) rows in a block's ring
+};
+// blocks of the launch on the current device = rows of [blocks, 2 dim] partial sums that it writes
+cudaError_t layer_bwd_blocks(const LayerBwdParams &p, int *blocks);
+cudaError_t launch_layer_bwd(const LayerBwdParams &p, float *partial, cudaStream_t st);
+
+// Heads whose columns are turned by their token's position.
+struct TurnParams {
+    const void *x;
+    int64_t x_token_stride, x_head_stride;
+    const int32_t *positions;
+    int64_t n_tokens;
+    int n_heads, half;  // pairs of a head
+    bool interleaved, inverse;
+    const float *rotation;  // [n_positions][2 half]: cosines, sines
+    int64_t n_positions;
+    void *out;
+    int64_t out_token_stride, out_head_stride;
+    Divider by_heads;
+};
+struct AppendParams {
+    const void *plain, *part;  // a row: plain_dim columns as they are, then 2 turn.half columns to turn
+    int64_t plain_stride, part_stride;
+    int plain_dim;
+    const int32_t *positions;
+    int64_t n_rows;
+    int dtype;
+    const int64_t *slots;
+    int64_t n_slots;
+    void *out;
+    int64_t out_stride;
+    int out_dtype;
+    float *scales;
+    TurnParams turn;  // the table, and the queries (n_tokens 0: none)
+};
+cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
+
 struct PageParams {
     const int32_t *before, *after;
     int n_req, ratio, page_size;

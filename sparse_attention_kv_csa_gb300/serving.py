@@ -1,4 +1,4 @@
-"""Serving the Compressor's rows: norm into a paged cache, page tables, attention over the cache.
+"""Serving the Compressor's rows: norms, append into a paged cache, page tables, attention over the cache.
 
 Argument checks and marshalling for the entry points of include/csa_serving.h; the arithmetic runs in the CUDA kernels
 of libcsa.so.  Ordinary calls (contiguous tensors, the current stream) go through csa_torch, which checks, allocates and
@@ -12,6 +12,12 @@ argument that does not fit, CSAError a call that the library refuses.
     grad_x, grad_weight       = rms_norm_backward(grad_out, h, weight, rstd, grad_residual=...)
     table, cu_rows, slots, counts = page_tables(before, after, ratio, page_size, free_pages, block_table, capacity)
     out, lse                  = latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, ...)
+    out, lse                  = shared_attention(q, cache, block_table, cu_q, seq_lens, cu_groups, shared_rows, ratio, scale, ...)
+    out, stream, mean, rstd   = layer_norm_forward(x, weight, bias, eps, residual=...)
+    grad_x, grad_weight, grad_bias = layer_norm_backward(grad_out, h, weight, mean, rstd, grad_residual=...)
+    out, scales, queries      = append_rows(rows, positions, rotation, slots, out, scales=..., rotary=..., queries=...)
+    out                       = rotate(x, positions, rotation, inverse=...)
+    rotation                  = rotation_table(n_positions, rot_dim)
 """
 from __future__ import annotations
 
@@ -21,8 +27,14 @@ import warnings
 
 from . import _build
 
-__all__ = ["csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention", "rms_norm_forward",
-           "rms_norm_backward", "page_tables", "latent_attention"]
+__all__ = ["csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention", "csa_layer_norm_fwd",
+           "csa_layer_norm_bwd", "csa_append_rows", "csa_rotate", "csa_shared_attention", "rms_norm_forward",
+           "rms_norm_backward", "page_tables", "latent_attention", "layer_norm_forward", "layer_norm_backward", "append_rows",
+           "rotate", "rotation_table", "shared_attention"]
+
+# the entry points that csa_torch calls, in the order of its bind()
+_ENTRIES = ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention", "csa_layer_norm_fwd",
+            "csa_layer_norm_bwd", "csa_append_rows", "csa_rotate", "csa_shared_attention")
 
 _lib = None
 _raise = None
@@ -45,7 +57,14 @@ def _bind(lib, check):
     lib.csa_page_tables.argtypes = [P, P, i32, i32, i32, P, i32, P, P, i64, i32, i64, P, P, P, P, P]
     lib.csa_latent_attention.argtypes = [P, i64, i64, P, i32, i64, i32, i32, i32, P, i64, i32, P, i64, i32, P, i64, i32,
                                          P, i32, f32, P, P, P, P]
-    for f in ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention"):
+    lib.csa_layer_norm_fwd.argtypes = [P, i64, P, i64, P, P, i64, i32, f32, i32, P, i64, P, P, P, P]
+    lib.csa_layer_norm_bwd.argtypes = [P, i64, P, i64, P, i64, P, P, P, i64, i32, i32, P, P, P, P]
+    lib.csa_append_rows.argtypes = [P, i64, i32, P, i64, i32, P, i64, i32, P, i64, i32, P, i64, P, i64, i32, P, P, i64, i64, P,
+                                    i64, i32, P, i64, i64, P]
+    lib.csa_rotate.argtypes = [P, i64, i64, P, i64, i32, i32, i32, P, i64, i32, i32, P, i64, i64, P]
+    lib.csa_shared_attention.argtypes = [P, i64, i64, P, i32, i64, i32, i32, i32, P, i64, i32, P, i64, i32, P, i64, i32,
+                                         P, P, P, i32, i32, f32, P, P, P, P]
+    for f in _ENTRIES:
         getattr(lib, f).restype = ctypes.c_int
     _lib, _raise = lib, check
 
@@ -58,8 +77,7 @@ def _load_torch():
         spec = importlib.util.spec_from_file_location("csa_torch", _build.build_binding())
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
-                      ("csa_rms_norm_fwd", "csa_rms_norm_bwd", "csa_page_tables", "csa_latent_attention")))
+        module.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in _ENTRIES))
         _short = module
     except Exception as e:  # no compiler or headers, or a library that this torch does not load
         warnings.warn("csa_torch is not to be had (%s): calls are checked and made in Python, some 8 us longer each"
@@ -140,6 +158,63 @@ def csa_latent_attention(q, q_token_stride, q_head_stride, cu_q, n_req, n_tokens
                                      head_dim, v_dim, _addr(cache), cache_stride, cache_dtype, _addr(row_scales),
                                      n_pages, page_size, _addr(block_table), table_stride, width, _addr(seq_lens),
                                      ratio, scale, _addr(sink), _addr(out), _addr(lse), _stream(stream)))
+
+
+def csa_layer_norm_fwd(x, x_stride, residual, residual_stride, weight, bias, n_rows, dim, eps, dtype, out, out_stride,
+                       residual_out, mean, rstd, stream=None) -> None:
+    _fit(32, dim=dim, dtype=dtype)
+    _fit(64, x_stride=x_stride, residual_stride=residual_stride, n_rows=n_rows, out_stride=out_stride)
+    _raise(_lib.csa_layer_norm_fwd(_addr(x), x_stride, _addr(residual), residual_stride, _addr(weight), _addr(bias), n_rows,
+                                   dim, eps, dtype, _addr(out), out_stride, _addr(residual_out), _addr(mean), _addr(rstd),
+                                   _stream(stream)))
+
+
+def csa_layer_norm_bwd(h, h_stride, grad_out, grad_out_stride, grad_residual, grad_residual_stride, weight, mean, rstd,
+                       n_rows, dim, dtype, grad_x, grad_weight, grad_bias, stream=None) -> None:
+    _fit(32, dim=dim, dtype=dtype)
+    _fit(64, h_stride=h_stride, grad_out_stride=grad_out_stride, grad_residual_stride=grad_residual_stride, n_rows=n_rows)
+    _raise(_lib.csa_layer_norm_bwd(_addr(h), h_stride, _addr(grad_out), grad_out_stride, _addr(grad_residual),
+                                   grad_residual_stride, _addr(weight), _addr(mean), _addr(rstd), n_rows, dim, dtype,
+                                   _addr(grad_x), _addr(grad_weight), _addr(grad_bias), _stream(stream)))
+
+
+def csa_append_rows(rows, row_stride, row_dim, rotary, rotary_stride, rot_dim, positions, n_rows, dtype, rotation,
+                    n_positions, interleaved, slots, n_slots, out, out_stride, out_dtype, scales, q, q_token_stride,
+                    q_head_stride, q_positions, n_tokens, n_heads, q_out, q_out_token_stride, q_out_head_stride,
+                    stream=None) -> None:
+    _fit(32, row_dim=row_dim, rot_dim=rot_dim, dtype=dtype, interleaved=interleaved, out_dtype=out_dtype, n_heads=n_heads)
+    _fit(64, row_stride=row_stride, rotary_stride=rotary_stride, n_rows=n_rows, n_positions=n_positions, n_slots=n_slots,
+         out_stride=out_stride, q_token_stride=q_token_stride, q_head_stride=q_head_stride, n_tokens=n_tokens,
+         q_out_token_stride=q_out_token_stride, q_out_head_stride=q_out_head_stride)
+    _raise(_lib.csa_append_rows(_addr(rows), row_stride, row_dim, _addr(rotary), rotary_stride, rot_dim, _addr(positions),
+                                n_rows, dtype, _addr(rotation), n_positions, interleaved, _addr(slots), n_slots, _addr(out),
+                                out_stride, out_dtype, _addr(scales), _addr(q), q_token_stride, q_head_stride,
+                                _addr(q_positions), n_tokens, n_heads, _addr(q_out), q_out_token_stride,
+                                q_out_head_stride, _stream(stream)))
+
+
+def csa_rotate(x, x_token_stride, x_head_stride, positions, n_tokens, n_heads, rot_dim, dtype, rotation, n_positions,
+               interleaved, inverse, out, out_token_stride, out_head_stride, stream=None) -> None:
+    _fit(32, n_heads=n_heads, rot_dim=rot_dim, dtype=dtype, interleaved=interleaved, inverse=inverse)
+    _fit(64, x_token_stride=x_token_stride, x_head_stride=x_head_stride, n_tokens=n_tokens, n_positions=n_positions,
+         out_token_stride=out_token_stride, out_head_stride=out_head_stride)
+    _raise(_lib.csa_rotate(_addr(x), x_token_stride, x_head_stride, _addr(positions), n_tokens, n_heads, rot_dim, dtype,
+                           _addr(rotation), n_positions, interleaved, inverse, _addr(out), out_token_stride,
+                           out_head_stride, _stream(stream)))
+
+
+def csa_shared_attention(q, q_token_stride, q_head_stride, cu_q, n_req, n_tokens, n_heads, head_dim, v_dim, cache,
+                         cache_stride, cache_dtype, row_scales, n_pages, page_size, block_table, table_stride, width,
+                         seq_lens, cu_groups, shared_rows, n_groups, ratio, scale, sink, out, lse, stream=None) -> None:
+    _fit(32, n_req=n_req, n_heads=n_heads, head_dim=head_dim, v_dim=v_dim, cache_dtype=cache_dtype, page_size=page_size,
+         width=width, n_groups=n_groups, ratio=ratio)
+    _fit(64, q_token_stride=q_token_stride, q_head_stride=q_head_stride, n_tokens=n_tokens, cache_stride=cache_stride,
+         n_pages=n_pages, table_stride=table_stride)
+    _raise(_lib.csa_shared_attention(_addr(q), q_token_stride, q_head_stride, _addr(cu_q), n_req, n_tokens, n_heads,
+                                     head_dim, v_dim, _addr(cache), cache_stride, cache_dtype, _addr(row_scales),
+                                     n_pages, page_size, _addr(block_table), table_stride, width, _addr(seq_lens),
+                                     _addr(cu_groups), _addr(shared_rows), n_groups, ratio, scale, _addr(sink),
+                                     _addr(out), _addr(lse), _stream(stream)))
 
 
 # ------------------------------------------------------------ checks
@@ -374,6 +449,15 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
         r = _short.latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim, row_scales, sink, out)
         if r is not None:
             return r if type(r) is tuple else _raise(r)
+    a, out, lse, d = _attention(q, cache, block_table, cu_q, seq_lens, ratio, v_dim, row_scales, sink, out, stream)
+    rc = _lib.csa_latent_attention(*a, ratio, scale, _pointer(sink), out.data_ptr(), lse.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
+    return out, lse
+
+
+def _attention(q, cache, block_table, cu_q, seq_lens, ratio, v_dim, row_scales, sink, out, stream):
+    """The attentions' common checks: (the entry points' arguments up to seq_lens, out, lse, the device's number)."""
     _fit(32, ratio=ratio, v_dim=0 if v_dim is None else v_dim)
     bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
     if type(q) is not _Tensor or q.dtype is not bf16 or q.dim() != 3:
@@ -417,11 +501,226 @@ def latent_attention(q, cache, block_table, cu_q, seq_lens, ratio, scale, v_dim=
     else:
         _check("out", out, bf16, (n, heads, v_dim), d)
     lse = _empty((n, heads), f32, device, stream)
-    rc = _lib.csa_latent_attention(q.data_ptr(), q_token if n > 1 else max(q_token, dim), q_head if heads > 1 else max(q_head, dim),
-                                   cu_q.data_ptr(), n_req, n, heads, dim, v_dim, cache.data_ptr(), row,
-                                   E4M3 if bits8 else BF16, _pointer(row_scales), pages, page_size, block_table.data_ptr(),
-                                   stride, width, seq_lens.data_ptr(), ratio, scale, _pointer(sink), out.data_ptr(),
-                                   lse.data_ptr(), _handle(stream, d))
+    return (q.data_ptr(), q_token if n > 1 else max(q_token, dim), q_head if heads > 1 else max(q_head, dim), cu_q.data_ptr(),
+            n_req, n, heads, dim, v_dim, cache.data_ptr(), row, E4M3 if bits8 else BF16, _pointer(row_scales), pages, page_size,
+            block_table.data_ptr(), stride, width, seq_lens.data_ptr()), out, lse, d
+
+
+def shared_attention(q, cache, block_table, cu_q, seq_lens, cu_groups, shared_rows, ratio, scale, v_dim=None, row_scales=None,
+                     sink=None, out=None, stream=None):
+    """latent_attention for a batch whose requests share prefixes, whose rows are read once a group.
+
+    cu_groups int32 [n_groups + 1]: requests [cu_groups[g], cu_groups[g+1]) have their first shared_rows[g] (int32
+    [n_groups]) rows in common; block_table lists those rows' pages for every request, the same pages or pages of equal
+    contents.  Everything else, and the result, as in latent_attention; see csa_shared_attention.
+    """
+    if _torch is None:
+        _load_torch()
+    if _short is not None and stream is None:
+        r = _short.shared_attention(q, cache, block_table, cu_q, seq_lens, cu_groups, shared_rows, ratio, scale, v_dim,
+                                    row_scales, sink, out)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
+    if not isinstance(q, _torch.Tensor):
+        raise TypeError("q must be a tensor")
+    d = _check_device(q, "q")
+    n_groups = _vector("cu_groups", cu_groups, _torch.int32, d) - 1
+    if n_groups < 0:
+        raise ValueError("cu_groups must be [n_groups + 1]")
+    _check("shared_rows", shared_rows, _torch.int32, (n_groups,), d)
+    _fit(32, n_groups=n_groups)
+    a, out, lse, d = _attention(q, cache, block_table, cu_q, seq_lens, ratio, v_dim, row_scales, sink, out, stream)
+    rc = _lib.csa_shared_attention(*a, cu_groups.data_ptr(), shared_rows.data_ptr(), n_groups, ratio, scale, _pointer(sink),
+                                   out.data_ptr(), lse.data_ptr(), _handle(stream, d))
     if rc:
         _raise(rc)
     return out, lse
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, stream=None):
+    """Layer norm of x [n_rows, dim] (bf16, f16 or f32; + residual), see csa_layer_norm_fwd.
+
+    weight, bias: fp32 [dim] or None (ones, zeros).  Returns (out, x + residual or None, mean fp32 [n_rows], rstd fp32
+    [n_rows]).
+    """
+    if _torch is None:
+        _load_torch()
+    if _short is not None and stream is None:
+        r = _short.layer_norm_forward(x, weight, bias, eps, residual, out)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
+    shape, code, d = _matrix("x", x)
+    n, dim = shape
+    _fit(32, dim=dim)
+    dtype, device, f32 = x.dtype, x.device, _torch.float32
+    xs = dim if x.is_contiguous() else _rows("x", x, dtype, shape, d)
+    rs = 0 if residual is None else _rows("residual", residual, dtype, shape, d)
+    if weight is not None:
+        _check("weight", weight, f32, (dim,), d)
+    if bias is not None:
+        _check("bias", bias, f32, (dim,), d)
+    if out is None:
+        out, out_stride = _empty(shape, dtype, device, stream), dim
+    else:
+        out_stride = _rows("out", out, dtype, tuple(shape), d)
+    total = None if residual is None else _empty(shape, dtype, device, stream)
+    mean, rstd = _empty((n,), f32, device, stream), _empty((n,), f32, device, stream)
+    rc = _lib.csa_layer_norm_fwd(x.data_ptr(), xs, _pointer(residual), rs, _pointer(weight), _pointer(bias), n, dim, eps, code,
+                                 out.data_ptr(), out_stride, _pointer(total), mean.data_ptr(), rstd.data_ptr(),
+                                 _handle(stream, d))
+    if rc:
+        _raise(rc)
+    return out, total, mean, rstd
+
+
+def layer_norm_backward(grad_out, h, weight, mean, rstd, grad_residual=None, stream=None):
+    """Gradient of layer_norm_forward: (grad_x [n_rows, dim] -- the residual's too --, grad_weight and grad_bias fp32 [dim]).
+
+    h is the forward's x + residual (x without a residual), mean and rstd its third and fourth result; grad_residual the
+    gradient that reaches x + residual directly.
+    """
+    if _torch is None:
+        _load_torch()
+    if _short is not None and stream is None:
+        r = _short.layer_norm_backward(grad_out, h, weight, mean, rstd, grad_residual)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
+    shape, code, d = _matrix("h", h)
+    n, dim = shape
+    _fit(32, dim=dim)
+    dtype, device, f32 = h.dtype, h.device, _torch.float32
+    hs = dim if h.is_contiguous() else _rows("h", h, dtype, shape, d)
+    gs = _rows("grad_out", grad_out, dtype, shape, d)
+    rs = 0 if grad_residual is None else _rows("grad_residual", grad_residual, dtype, shape, d)
+    if weight is not None:
+        _check("weight", weight, f32, (dim,), d)
+    _check("mean", mean, f32, (n,), d)
+    _check("rstd", rstd, f32, (n,), d)
+    grad_x = _empty(shape, dtype, device, stream)
+    grad_weight, grad_bias = _empty((dim,), f32, device, stream), _empty((dim,), f32, device, stream)
+    rc = _lib.csa_layer_norm_bwd(h.data_ptr(), hs, grad_out.data_ptr(), gs, _pointer(grad_residual), rs, _pointer(weight),
+                                 mean.data_ptr(), rstd.data_ptr(), n, dim, code, grad_x.data_ptr(), grad_weight.data_ptr(),
+                                 grad_bias.data_ptr(), _handle(stream, d))
+    if rc:
+        _raise(rc)
+    return grad_x, grad_weight, grad_bias
+
+
+def rotation_table(n_positions, rot_dim, base=10000.0, device=None):
+    """The table that append_rows and rotate read: fp32 [n_positions, rot_dim], cosines of the rot_dim / 2 pairs' angles
+    position * base^(-2 i / rot_dim), then their sines.  Angles are formed and reduced in 64 bits.  Made once by a program;
+    any other table of that shape does too (scaled frequencies, positions of its own)."""
+    import torch
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2 (got %s)" % (rot_dim,))
+    if n_positions < 0:
+        raise ValueError("n_positions must be >= 0 (got %s)" % (n_positions,))
+    if not base > 0:
+        raise ValueError("base must be positive (got %s)" % (base,))
+    device = "cuda" if device is None else device
+    half = rot_dim // 2
+    at = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None]
+    at = at * base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    return torch.cat([at.cos(), at.sin()], 1).float()
+
+
+def _heads(name, t, dtype, shape, device):
+    """(token stride, head stride) of a [n_tokens, n_heads, rot_dim] tensor whose last dimension is contiguous."""
+    _fits(name, t, dtype, shape, device)
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError("%s's last dimension must be contiguous" % name)
+    n, heads, rot = t.shape
+    return t.stride(0) if n > 1 else max(t.stride(0), rot), t.stride(1) if heads > 1 else max(t.stride(1), rot)
+
+
+def append_rows(rows, positions, rotation, slots, out, scales=None, rotary=None, interleaved=False, queries=None,
+                query_positions=None, query_out=None, stream=None):
+    """Rows to the slots of a paged cache, their last rot_dim columns rotated by position; see csa_append_rows.
+
+    rows [n_rows, row_dim] (bf16, f16 or f32), rotated in their last rot_dim columns, or with rotary [n_rows, rot_dim] kept as
+    they are and followed by the rotation of rotary; positions int32 [n_rows]; rotation fp32 [n_positions, rot_dim]
+    (rotation_table); slots int64 [n_rows]; out [n_slots, width] in rows' type, or torch.float8_e4m3fn with scales fp32
+    [n_slots].  queries [n_tokens, n_heads, rot_dim] (a view of the heads' rotated columns, say) are rotated beside them by
+    query_positions (positions by default) into query_out (a new tensor by default; queries itself to rotate in place).
+    Returns (out, scales, query_out).
+    """
+    if _torch is None:
+        _load_torch()
+    if _short is not None and stream is None:
+        r = _short.append_rows(rows, positions, rotation, slots, out, scales, rotary, interleaved, queries, query_positions,
+                               query_out)
+        if r is not None:
+            return r if type(r) is tuple else _raise(r)
+    shape, code, d = _matrix("rows", rows)
+    n, row_dim = shape
+    _fit(32, dim=row_dim)
+    dtype, device, f32, i32 = rows.dtype, rows.device, _torch.float32, _torch.int32
+    row_stride = _rows("rows", rows, dtype, tuple(shape), d)
+    _check("positions", positions, i32, (n,), d)
+    _check("rotation", rotation, f32, (None, None), d)
+    n_positions, rot = rotation.shape
+    _fit(32, rot_dim=rot)
+    rotary_stride = 0 if rotary is None else _rows("rotary", rotary, dtype, (n, rot), d)
+    width = row_dim + (0 if rotary is None else rot)
+    _check("slots", slots, _torch.int64, (n,), d)
+    if not isinstance(out, _torch.Tensor):
+        raise TypeError("out must be a tensor")
+    bits8 = out.dtype == _torch.float8_e4m3fn
+    out_stride = _rows("out", out, out.dtype if bits8 else dtype, (None, width), d)
+    if bits8 != (scales is not None):
+        raise ValueError("scales go with a float8_e4m3fn out, and it with them")
+    if bits8:
+        _check("scales", scales, f32, (out.shape[0],), d)
+    q_args = (None, 0, 0, None, 0, 1, None, 0, 0)
+    if queries is None:
+        if query_positions is not None or query_out is not None:
+            raise ValueError("query_positions and query_out go with queries")
+    else:
+        qt, qh = _heads("queries", queries, dtype, (None, None, rot), d)
+        tokens, heads = queries.shape[:2]
+        _fit(32, n_heads=heads)
+        query_positions = positions if query_positions is None else query_positions
+        _check("query_positions", query_positions, i32, (tokens,), d)
+        if query_out is None:
+            query_out = _empty((tokens, heads, rot), dtype, device, stream)
+        ot, oh = _heads("query_out", query_out, dtype, (tokens, heads, rot), d)
+        q_args = (queries.data_ptr(), qt, qh, query_positions.data_ptr(), tokens if heads else 0, max(heads, 1),
+                  query_out.data_ptr(), ot, oh)
+    rc = _lib.csa_append_rows(rows.data_ptr(), row_stride, row_dim, _pointer(rotary), rotary_stride, rot, positions.data_ptr(), n,
+                              code, rotation.data_ptr(), n_positions, bool(interleaved), slots.data_ptr(), out.shape[0],
+                              out.data_ptr(), out_stride, E4M3 if bits8 else code, _pointer(scales), *q_args,
+                              _handle(stream, d))
+    if rc:
+        _raise(rc)
+    return out, scales, query_out
+
+
+def rotate(x, positions, rotation, interleaved=False, inverse=False, out=None, stream=None):
+    """Rotation of x [n_tokens, n_heads, rot_dim] (bf16, f16 or f32; any strides but the last) by the tokens' positions, or
+    its inverse; see csa_rotate.  out: where the result goes (x itself in place), a new tensor by default.  Returns out."""
+    if _torch is None:
+        _load_torch()
+    if _short is not None and stream is None:
+        r = _short.rotate(x, positions, rotation, interleaved, inverse, out)
+        if r is not None:
+            return r if type(r) is not int else _raise(r)
+    if not isinstance(x, _torch.Tensor):
+        raise TypeError("x must be a tensor")
+    code = _CODES.get(x.dtype, E4M3)
+    if code == E4M3 or x.dim() != 3:
+        raise ValueError("x must be [n_tokens, n_heads, rot_dim] in bf16, f16 or f32 (got %s, %s)" % (tuple(x.shape), x.dtype))
+    d = _check_device(x, "x")
+    n, heads, rot = x.shape
+    _fit(32, n_heads=heads, rot_dim=rot)
+    xt, xh = _heads("x", x, x.dtype, (n, heads, rot), d)
+    _check("positions", positions, _torch.int32, (n,), d)
+    _check("rotation", rotation, _torch.float32, (None, rot), d)
+    if out is None:
+        out = _empty((n, heads, rot), x.dtype, x.device, stream)
+    ot, oh = _heads("out", out, x.dtype, (n, heads, rot), d)
+    rc = _lib.csa_rotate(x.data_ptr(), xt, xh, positions.data_ptr(), n if heads else 0, max(heads, 1), rot, code,
+                         rotation.data_ptr(), rotation.shape[0], bool(interleaved), bool(inverse), out.data_ptr(), ot, oh,
+                         _handle(stream, d))
+    if rc:
+        _raise(rc)
+    return out
