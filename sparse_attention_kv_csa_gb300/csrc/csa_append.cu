@@ -18,37 +18,67 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kHeadsAThread = 4;
 
-// Cosines and sines of pairs [i, i + N) of a position, NaN where the table has no such position.
+// Cosines and sines of pairs [i, i + N) of a position, NaN where the table has no such position.  With N > 1 i, the table's rows
+// and its base are whole vectors of min(N, 4) floats.
 template <int N> __device__ __forceinline__ void angles(const TurnParams &p, int position, int i, float (&cos)[N], float (&sin)[N])
 {
     const bool have = position >= 0 && position < p.n_positions;
-    const float *row = p.rotation + (int64_t)(have ? position : 0) * 2 * p.half;
+    const float *row = p.rotation + (int64_t)(have ? position : 0) * 2 * p.half + i;
+    auto get = [&](const float *at, float (&v)[N]) {
+        if constexpr (N >= 4) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(at + k));
+                v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+            }
+        } else if constexpr (N == 2) {
+            const float2 f = __ldg(reinterpret_cast<const float2 *>(at));
+            v[0] = f.x, v[1] = f.y;
+        } else {
+            v[0] = __ldg(at);
+        }
+    };
+    if (p.n_positions > 0) {
+        get(row, cos);
+        get(row + p.half, sin);
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        cos[k] = have ? __ldg(row + i + k) : __int_as_float(0x7fffffff);
-        sin[k] = have ? __ldg(row + p.half + i + k) : __int_as_float(0x7fffffff);
+        cos[k] = have ? cos[k] : __int_as_float(0x7fffffff);
+        sin[k] = have ? (p.inverse ? -sin[k] : sin[k]) : __int_as_float(0x7fffffff);
     }
-    if (p.inverse)
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            sin[k] = -sin[k];
 }
 
-template <typename T, int VEC> __device__ __forceinline__ void read(const T *p, float (&v)[VEC])
+// a cos - b sin and a sin + b cos
+__device__ __forceinline__ float2 turn(float a, float b, float cos, float sin)
 {
-    const Pack<T, VEC> a = *reinterpret_cast<const Pack<T, VEC> *>(p);
-    unpack(a, v);
+    return make_float2(fmaf(a, cos, -(b * sin)), fmaf(a, sin, b * cos));
 }
 
-// VEC: elements of a vector (16 bytes), or 1; NV: vectors a lane
-template <typename T, bool BITS8, int VEC, int NV> __device__ void append_row(const AppendParams &p, int64_t row)
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> read(const T *p) { return *reinterpret_cast<const Pack<T, VEC> *>(p); }
+
+// VEC: elements of a vector (16 bytes), or 1; NV: vectors a lane.  Everything that does not hang on another load is read before
+// anything is used: a row is some microsecond of latency, and a row's own loads are all that a warp has under way.
+template <typename T, bool BITS8, int VEC, int NV> __device__ __forceinline__ void append_row(const AppendParams &p, int64_t row)
 {
     const int lane = threadIdx.x & 31, half = p.turn.half, width = p.plain_dim + 2 * half;
+    const T *plain = static_cast<const T *>(p.plain) + row * p.plain_stride, *part = static_cast<const T *>(p.part) + row * p.part_stride;
     const int64_t to = __ldg(p.slots + row);
+    const int position = __ldg(p.positions + row);
+    // the vector of the part that lane's vector i is turned with, when pairs are half the part apart
+    auto partner = [&](int j) { return j < half ? j + half : j - half; };
+    Pack<T, VEC> in[NV], with[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC, j = c - p.plain_dim;
+        if (c < width) {
+            in[i] = read<T, VEC>(j < 0 ? plain + c : part + j);
+            if (j >= 0 && (VEC == 1 || !p.turn.interleaved))
+                with[i] = read<T, VEC>(part + (p.turn.interleaved ? j ^ 1 : partner(j)));
+        }
+    }
     if (to < 0 || to >= p.n_slots)
         return;
-    const int position = __ldg(p.positions + row);
-    const T *plain = static_cast<const T *>(p.plain) + row * p.plain_stride, *part = static_cast<const T *>(p.part) + row * p.part_stride;
     float v[NV][VEC];
     float amax = 0.0f;
 #pragma unroll
@@ -56,35 +86,27 @@ template <typename T, bool BITS8, int VEC, int NV> __device__ void append_row(co
         const int c = (i * 32 + lane) * VEC, j = c - p.plain_dim;
         if (c >= width)
             continue;
-        if (j < 0) {
-            read<T, VEC>(plain + c, v[i]);
-        } else {
-            read<T, VEC>(part + j, v[i]);
-            if (p.turn.interleaved) {
+        unpack(in[i], v[i]);
+        if (j >= 0) {
+            if (VEC > 1 && p.turn.interleaved) {
                 if constexpr (VEC > 1) {
                     float cos[VEC / 2], sin[VEC / 2];
                     angles(p.turn, position, j / 2, cos, sin);
 #pragma unroll
                     for (int k = 0; k < VEC / 2; ++k) {
-                        const float a = v[i][2 * k], b = v[i][2 * k + 1];
-                        v[i][2 * k] = a * cos[k] - b * sin[k];
-                        v[i][2 * k + 1] = a * sin[k] + b * cos[k];
+                        const float2 t = turn(v[i][2 * k], v[i][2 * k + 1], cos[k], sin[k]);
+                        v[i][2 * k] = t.x;
+                        v[i][2 * k + 1] = t.y;
                     }
-                } else {
-                    float cos[1], sin[1];
-                    angles(p.turn, position, j / 2, cos, sin);
-                    const float u = Elem<T>::to(part[j ^ 1]);
-                    v[i][0] = j & 1 ? u * sin[0] + v[i][0] * cos[0] : v[i][0] * cos[0] - u * sin[0];
                 }
             } else {
-                const bool upper = j >= half;
-                const int pair = upper ? j - half : j;
+                const bool upper = p.turn.interleaved ? j & 1 : j >= half;
                 float u[VEC], cos[VEC], sin[VEC];
-                read<T, VEC>(part + (upper ? pair : pair + half), u);
-                angles(p.turn, position, pair, cos, sin);
+                unpack(with[i], u);
+                angles(p.turn, position, p.turn.interleaved ? j / 2 : upper ? j - half : j, cos, sin);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
-                    v[i][k] = upper ? u[k] * sin[k] + v[i][k] * cos[k] : v[i][k] * cos[k] - u[k] * sin[k];
+                    v[i][k] = upper ? turn(u[k], v[i][k], cos[k], sin[k]).y : turn(v[i][k], u[k], cos[k], sin[k]).x;
             }
         }
         if constexpr (BITS8)
@@ -139,123 +161,143 @@ template <typename T, bool BITS8, int VEC, int NV> __device__ void append_row(co
 
 // Heads: unit u of a head is its vector u (pairs of neighbours), or the vectors u and u + units (pairs half a part apart); with
 // VEC 1 a unit is a pair.
-template <typename T, int VEC> __device__ void turn_heads(const TurnParams &p, int64_t block)
+template <typename T, int VEC, bool NEIGHBOURS> __device__ __forceinline__ void turn_heads(const TurnParams &p, int64_t block)
 {
-    constexpr int N = VEC;  // values of each of a and b in the halves' form; neighbours have N / 2 pairs
-    const int units = VEC == 1 ? p.half : p.interleaved ? 2 * p.half / VEC : p.half / VEC;
-    const int rows = kThreads / units > 0 ? kThreads / units : 1;  // (a part of more units than threads takes several turns)
+    constexpr bool kOne = VEC > 1 && NEIGHBOURS;  // a and b lie in one vector
+    constexpr int N = kOne ? VEC / 2 : VEC;       // pairs of a unit
+    const int units = p.half / N;
+    const int rows = units < kThreads ? kThreads / units : 1;  // heads side by side (a part of more units than threads takes several turns)
+    const int64_t end = p.n_tokens * p.n_heads;
     for (int first = 0; first < units; first += kThreads) {
         const int u = first + (units > kThreads ? (int)threadIdx.x : (int)threadIdx.x % units);
         const int sub = units > kThreads ? 0 : (int)threadIdx.x / units;
         if (u >= units || sub >= rows)
             continue;
-        const int at_a = VEC == 1 && p.interleaved ? 2 * u : u * VEC, at_b = VEC == 1 && p.interleaved ? 2 * u + 1 : u * VEC + p.half;
-        const int pair = VEC > 1 && p.interleaved ? u * VEC / 2 : u * VEC;
-        float a[kHeadsAThread][N], b[kHeadsAThread][N];
+        const int at_a = NEIGHBOURS ? 2 * N * u : N * u, at_b = NEIGHBOURS ? 2 * u + 1 : N * u + p.half;
+        Pack<T, VEC> a[kHeadsAThread], b[kHeadsAThread];
         int position[kHeadsAThread];
-        int64_t row[kHeadsAThread];
-        const bool neighbours = VEC > 1 && p.interleaved;
+        int64_t to[kHeadsAThread];
 #pragma unroll
         for (int k = 0; k < kHeadsAThread; ++k) {
-            row[k] = (block * kHeadsAThread + k) * rows + sub;
-            if (row[k] < p.n_tokens * p.n_heads) {
-                const uint32_t token = p.by_heads.quotient((uint32_t)row[k]), head = p.by_heads.remainder((uint32_t)row[k]);
+            const int64_t row = (block * kHeadsAThread + k) * rows + sub;
+            to[k] = -1;
+            if (row < end) {
+                const uint32_t token = p.by_heads.quotient((uint32_t)row), head = (uint32_t)row - token * (uint32_t)p.n_heads;
                 position[k] = __ldg(p.positions + token);
+                to[k] = (int64_t)token * p.out_token_stride + (int64_t)head * p.out_head_stride;
                 const T *src = static_cast<const T *>(p.x) + (int64_t)token * p.x_token_stride + (int64_t)head * p.x_head_stride;
-                read<T, VEC>(src + at_a, a[k]);
-                if (!neighbours)
-                    read<T, VEC>(src + at_b, b[k]);
+                a[k] = read<T, VEC>(src + at_a);
+                if (!kOne)
+                    b[k] = read<T, VEC>(src + at_b);
             }
         }
 #pragma unroll
         for (int k = 0; k < kHeadsAThread; ++k) {
-            if (row[k] >= p.n_tokens * p.n_heads)
+            if (to[k] < 0)
                 continue;
-            const uint32_t token = p.by_heads.quotient((uint32_t)row[k]), head = p.by_heads.remainder((uint32_t)row[k]);
-            T *dst = static_cast<T *>(p.out) + (int64_t)token * p.out_token_stride + (int64_t)head * p.out_head_stride;
-            if (neighbours) {
-                if constexpr (VEC > 1) {
-                    float cos[VEC / 2], sin[VEC / 2];
-                    angles(p, position[k], pair, cos, sin);
-#pragma unroll
-                    for (int i = 0; i < VEC / 2; ++i) {
-                        const float x = a[k][2 * i], y = a[k][2 * i + 1];
-                        a[k][2 * i] = x * cos[i] - y * sin[i];
-                        a[k][2 * i + 1] = x * sin[i] + y * cos[i];
-                    }
-                    store<T, VEC>(dst + at_a, pack<T, VEC>(a[k]));
-                }
-            } else {
-                float cos[N], sin[N];
-                angles(p, position[k], pair, cos, sin);
+            T *dst = static_cast<T *>(p.out) + to[k];
+            float x[VEC], cos[N], sin[N];
+            angles(p, position[k], N * u, cos, sin);
+            unpack(a[k], x);
+            if constexpr (kOne) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float x = a[k][i], y = b[k][i];
-                    a[k][i] = x * cos[i] - y * sin[i];
-                    b[k][i] = x * sin[i] + y * cos[i];
+                    const float2 t = turn(x[2 * i], x[2 * i + 1], cos[i], sin[i]);
+                    x[2 * i] = t.x;
+                    x[2 * i + 1] = t.y;
                 }
-                store<T, VEC>(dst + at_a, pack<T, VEC>(a[k]));
-                store<T, VEC>(dst + at_b, pack<T, VEC>(b[k]));
+            } else {
+                float y[VEC];
+                unpack(b[k], y);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float2 t = turn(x[i], y[i], cos[i], sin[i]);
+                    x[i] = t.x;
+                    y[i] = t.y;
+                }
+                store<T, VEC>(dst + at_b, pack<T, VEC>(y));
             }
+            store<T, VEC>(dst + at_a, pack<T, VEC>(x));
         }
     }
 }
 
-// The first blocks take rows, the others heads.  VEC, NV: of the rows; HVEC: of the heads.
-template <typename T, bool BITS8, int VEC, int NV, int HVEC>
+enum Heads { kNone, kScalar, kHalves, kNeighbours };  // heads to turn: none, pair by pair, in vectors of either form
+
+// The first blocks take rows (NV 0: there are none), the others heads.  Forms apart, so that rows alone or heads alone do not run
+// with the registers of both (65543 rows of 512: 54 registers a thread against 92).
+template <typename T, bool BITS8, int VEC, int NV, Heads HEADS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p, int row_blocks)
 {
+    constexpr int V = 16 / sizeof(T);
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x < row_blocks) {
-        const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-        if (row < p.n_rows)
-            append_row<T, BITS8, VEC, NV>(p, row);
-    } else {
-        turn_heads<T, HVEC>(p.turn, blockIdx.x - row_blocks);
+    if constexpr (NV > 0)
+        if (blockIdx.x < row_blocks) {
+            const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+            if (row < p.n_rows)
+                append_row<T, BITS8, VEC, NV>(p, row);
+            return;
+        }
+    if constexpr (HEADS == kScalar) {
+        if (p.turn.interleaved)
+            turn_heads<T, 1, true>(p.turn, blockIdx.x - row_blocks);
+        else
+            turn_heads<T, 1, false>(p.turn, blockIdx.x - row_blocks);
+    } else if constexpr (HEADS != kNone) {
+        turn_heads<T, V, HEADS == kNeighbours>(p.turn, blockIdx.x - row_blocks);
     }
 }
 
-template <typename T, bool BITS8, int VEC, int NV, int HVEC> cudaError_t go(const AppendParams &p, cudaStream_t st)
+template <typename T, bool BITS8, int VEC, int NV, Heads HEADS> cudaError_t go(const AppendParams &p, cudaStream_t st)
 {
-    const int row_blocks = (int)((p.n_rows + kThreads / 32 - 1) / (kThreads / 32));
-    const int units = HVEC == 1 ? p.turn.half : p.turn.interleaved ? 2 * p.turn.half / HVEC : p.turn.half / HVEC;
-    const int64_t rows = (int64_t)(kThreads / units > 0 ? kThreads / units : 1) * kHeadsAThread;
-    const int64_t heads = p.turn.n_tokens * p.turn.n_heads;
-    return launch_pdl(append_kernel<T, BITS8, VEC, NV, HVEC>, dim3((unsigned)(row_blocks + (heads + rows - 1) / rows)), dim3(kThreads), 0, st,
-                      p, row_blocks);
+    constexpr int N = HEADS == kScalar ? 1 : HEADS == kNeighbours ? 8 / (int)sizeof(T) : 16 / (int)sizeof(T);
+    const int64_t row_blocks = (p.n_rows + kThreads / 32 - 1) / (kThreads / 32);
+    const int units = p.turn.half / N;
+    const int64_t rows = (int64_t)(units < kThreads ? kThreads / units : 1) * kHeadsAThread;
+    const int64_t heads = HEADS == kNone ? 0 : p.turn.n_tokens * p.turn.n_heads;
+    return launch_pdl(append_kernel<T, BITS8, VEC, NV, HEADS>, dim3((unsigned)(row_blocks + (heads + rows - 1) / rows)), dim3(kThreads), 0, st,
+                      p, (int)row_blocks);
 }
 
-template <typename T, bool BITS8, int VEC, int NV> cudaError_t go_heads(const AppendParams &p, bool head_vectors, cudaStream_t st)
+template <typename T, bool BITS8, int VEC, int NV> cudaError_t go_heads(const AppendParams &p, Heads heads, cudaStream_t st)
 {
-    return head_vectors ? go<T, BITS8, VEC, NV, 16 / sizeof(T)>(p, st) : go<T, BITS8, VEC, NV, 1>(p, st);
+    if constexpr (NV > 0)
+        if (heads == kNone)
+            return go<T, BITS8, VEC, NV, kNone>(p, st);
+    return heads == kScalar     ? go<T, BITS8, VEC, NV, kScalar>(p, st)
+           : heads == kHalves ? go<T, BITS8, VEC, NV, kHalves>(p, st)
+                              : go<T, BITS8, VEC, NV, kNeighbours>(p, st);
 }
 
-template <typename T, bool BITS8> cudaError_t go_rows(const AppendParams &p, bool row_vectors, bool head_vectors, cudaStream_t st)
+template <typename T, bool BITS8> cudaError_t go_rows(const AppendParams &p, bool vectors, Heads heads, cudaStream_t st)
 {
     constexpr int V = 16 / sizeof(T);
-    const int width = p.n_rows ? p.plain_dim + 2 * p.turn.half : 1;
-    if (row_vectors) {
-        if (width <= 32 * V) return go_heads<T, BITS8, V, 1>(p, head_vectors, st);
-        if (width <= 64 * V) return go_heads<T, BITS8, V, 2>(p, head_vectors, st);
-        if (width <= 96 * V) return go_heads<T, BITS8, V, 3>(p, head_vectors, st);
-        if (V == 8 || width <= 128 * V) return go_heads<T, BITS8, V, 4>(p, head_vectors, st);
-        return go_heads<T, BITS8, V, 8>(p, head_vectors, st);
-    }
-    return go_heads<T, BITS8, 1, 32>(p, head_vectors, st);
+    const int width = p.plain_dim + 2 * p.turn.half;
+    if (!vectors)
+        return go_heads<T, BITS8, 1, 32>(p, heads, st);
+    if (width <= 32 * V) return go_heads<T, BITS8, V, 1>(p, heads, st);
+    if (width <= 64 * V) return go_heads<T, BITS8, V, 2>(p, heads, st);
+    if (width <= 96 * V) return go_heads<T, BITS8, V, 3>(p, heads, st);
+    if constexpr (V == 4)  // (1024 columns of 16 bits are 128 vectors)
+        if (width > 128 * V) return go_heads<T, BITS8, V, 8>(p, heads, st);
+    return go_heads<T, BITS8, V, 4>(p, heads, st);
 }
 
 template <typename T> cudaError_t go_type(const AppendParams &p, cudaStream_t st)
 {
     constexpr int v = 16 / sizeof(T);
     const TurnParams &t = p.turn;
-    const bool pairs = t.interleaved ? 2 * t.half % v == 0 : t.half % v == 0;
-    const bool rows = p.n_rows == 0 || (pairs && p.plain_dim % v == 0 && (p.plain_dim == 0 || (on(p.plain, 16) && p.plain_stride % v == 0)) &&
-                                        on(p.part, 16) && p.part_stride % v == 0 && p.out_stride % v == 0 &&
-                                        on(p.out, v * elem_bytes(p.out_dtype)));
-    const bool heads = t.n_tokens == 0 || (pairs && on(t.x, 16) && on(t.out, 16) && t.x_token_stride % v == 0 && t.x_head_stride % v == 0 &&
-                                           t.out_token_stride % v == 0 && t.out_head_stride % v == 0);
-    return p.out_dtype == CSA_DTYPE_E4M3 ? go_rows<T, true>(p, rows, heads, st) : go_rows<T, false>(p, rows, heads, st);
+    // whole vectors of pairs, and of their angles
+    const bool pairs = (t.interleaved ? 2 * t.half % v == 0 : t.half % v == 0) && t.half % 4 == 0 && on(t.rotation, 16);
+    const bool in_vectors = pairs && on(t.x, 16) && on(t.out, 16) && t.x_token_stride % v == 0 && t.x_head_stride % v == 0 &&
+                            t.out_token_stride % v == 0 && t.out_head_stride % v == 0;
+    const Heads heads = t.n_tokens == 0 ? kNone : !in_vectors ? kScalar : t.interleaved ? kNeighbours : kHalves;
+    if (p.n_rows == 0)
+        return go_heads<T, false, v, 0>(p, heads, st);
+    const bool vectors = pairs && p.plain_dim % v == 0 && (p.plain_dim == 0 || (on(p.plain, 16) && p.plain_stride % v == 0)) &&
+                         on(p.part, 16) && p.part_stride % v == 0 && p.out_stride % v == 0 && on(p.out, v * elem_bytes(p.out_dtype));
+    return p.out_dtype == CSA_DTYPE_E4M3 ? go_rows<T, true>(p, vectors, heads, st) : go_rows<T, false>(p, vectors, heads, st);
 }
 
 }  // namespace
