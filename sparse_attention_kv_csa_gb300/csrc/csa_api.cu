@@ -366,7 +366,8 @@ cudaError_t make_tensor_map_parts(CUtensorMap *m, const void *ptr, int64_t C, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups)
+cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups,
+                                   int box_chunks)
 {
     cudaError_t e;
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn(&e);
@@ -376,7 +377,7 @@ cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows
         return cudaErrorInvalidValue;
     const cuuint64_t dims[4] = {64, 8, (cuuint64_t)chunks, (cuuint64_t)rows / 8};
     const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, 128, (cuuint64_t)stride * 16};
-    const cuuint32_t box[4] = {64, 8, (cuuint32_t)chunks, (cuuint32_t)groups};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(box_chunks ? box_chunks : chunks), (cuuint32_t)groups};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -69,12 +69,12 @@ struct Segment {
     bool some;
 };
 
-CSA_BOTH Segment segment_of(int nt, int off, long long left)
+CSA_BOTH Segment segment_of(int nt, int off, long long left, int head = kHead)
 {
     Segment s;
-    s.take = (int)min((long long)(nt + kHead - off), left);
-    s.t0 = max(off - kHead, 0);
-    s.t1 = max(off + s.take - kHead, 0);
+    s.take = (int)min((long long)(nt + head - off), left);
+    s.t0 = max(off - head, 0);
+    s.t1 = max(off + s.take - head, 0);
     s.some = s.t1 > s.t0 || (nt == 0 && off == 0);
     return s;
 }

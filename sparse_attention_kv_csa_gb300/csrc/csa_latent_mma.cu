@@ -28,11 +28,15 @@
 // Work is cut evenly: an item counts three units for its queries and output and one for each tile; block c takes the units
 // [c T / G, (c+1) T / G) of the T units.  Items that cross a cut leave (O, m, l) of their parts in the workspace and a
 // second kernel joins them in order.  Nothing else depends on the grid, and no order on timing.
+//
+// SHARED: a request's first rows may be dealt with apart, as a prefix that it shares (csa_shared.cu).  Its rows here are those
+// behind; every item leaves its parts, which csa_shared.cu joins with the prefix's.
 #include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "csa_launch.h"
 #include "csa_serving_launch.h"
+#include "csa_shared.cuh"
 #include "csa_tcgen05.cuh"
 
 namespace csa {
@@ -81,7 +85,7 @@ struct Shared {
     uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[kScores], p_full[2], q_full, q_empty, flags, drained;
     long long sums[16];
     long long total;
-    int r, m, off;               // where the block's units begin
+    int r, m, off, index;        // where the block's units begin; the item's number in all
     int first[4];                // and the facts of request r
     uint32_t tmem;
     alignas(16) float scales[kMaxStages][64];
@@ -97,7 +101,20 @@ struct Request {
     int items;
 };
 
-__device__ __forceinline__ Request request(const AttnParams &p, int r)
+struct NoPrefix {};
+template <bool SHARED> struct PrefixOf {
+    using type = NoPrefix;
+};
+template <> struct PrefixOf<true> {
+    using type = SharedPlan;
+};
+template <bool SHARED> using Prefix = typename PrefixOf<SHARED>::type;
+
+// The rows of request r that its group's prefix part has (whole pages), and the group.
+__device__ __forceinline__ int2 own_of(const NoPrefix &, int) { return make_int2(0, -1); }
+__device__ __forceinline__ int2 own_of(const SharedPlan &s, int r) { return s.own[r]; }
+
+template <bool SHARED> __device__ __forceinline__ Request request(const AttnParams &p, const Prefix<SHARED> &prefix, int r)
 {
     Request q;
     q.first = max(__ldg(p.cu_q + r), 0);
@@ -105,6 +122,8 @@ __device__ __forceinline__ Request request(const AttnParams &p, int r)
     q.nq = (int)max(end - q.first, (int64_t)0);
     q.before = __ldg(p.seq_lens + r) - (__ldg(p.cu_q + r + 1) - q.first);
     q.items = (int)(((int64_t)q.nq * p.n_heads + kTile - 1) / kTile);
+    if constexpr (SHARED)
+        q.before -= own_of(prefix, r).x * p.ratio;  // (the prefix part has no more rows than every new token sees)
     return q;
 }
 
@@ -127,14 +146,15 @@ template <int R> __device__ __forceinline__ int item_tiles(const AttnParams &p, 
 }
 
 // The block's segments, walked alike by every role.
-template <int R> struct Walk {
+template <bool SHARED, int R> struct Walk {
     const AttnParams &p;
+    const Prefix<SHARED> &prefix;
     Request q;
     int r, m, off;
     long long left;
-    int nt, t0, t1;
-    __device__ Walk(const AttnParams &p_, const Shared &s, long long units)
-        : p(p_), q{s.first[0], s.first[1], s.first[2], s.first[3]}, r(s.r), m(s.m), off(s.off), left(units)
+    int nt, t0, t1, index;
+    __device__ Walk(const AttnParams &p_, const Prefix<SHARED> &prefix_, const Shared &s, long long units)
+        : p(p_), prefix(prefix_), q{s.first[0], s.first[1], s.first[2], s.first[3]}, r(s.r), m(s.m), off(s.off), left(units), index(s.index - 1)
     {
     }
     // the next segment: tiles [t0, t1) of item (r, m); nt == 0 (t0 == t1) is an item that sees nothing
@@ -145,7 +165,7 @@ template <int R> struct Walk {
                 if (++r >= p.n_req)
                     return false;
                 m = 0;
-                q = request(p, r);
+                q = request<SHARED>(p, prefix, r);
             }
             nt = item_tiles<R>(p, q, m);
             const Segment s = segment_of(nt, off, left);
@@ -154,12 +174,21 @@ template <int R> struct Walk {
             left -= s.take;
             off = 0;
             ++m;
+            ++index;
             if (s.some)
                 return true;
         }
         return false;
     }
     __device__ int item() const { return m - 1; }
+    // The request's pages behind its prefix.
+    __device__ const int32_t *table() const
+    {
+        const int32_t *t = p.block_table + (int64_t)r * p.table_stride;
+        if constexpr (SHARED)
+            t += p.by_page.quotient((uint32_t)own_of(prefix, r).x);
+        return t;
+    }
 };
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
@@ -190,9 +219,9 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two)
     return f2_to_bf16x2(__half22float2(*reinterpret_cast<const __half2 *>(&h)));
 }
 
-template <Rows ROWS, int NK, int R>
+template <bool SHARED, Rows ROWS, int NK, int R>
 __global__ void __launch_bounds__(kThreadsOf<ROWS, NK>, per_sm(ROWS, NK))
-latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant__ CUtensorMap boxes,
+latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> prefix, const __grid_constant__ CUtensorMap boxes,
                   const __grid_constant__ CUtensorMap groups, unsigned *status)
 {
     constexpr int kThreads = kThreadsOf<ROWS, NK>;
@@ -233,7 +262,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
     // units over equal stretches of items, a stretch a thread
     int *items = reinterpret_cast<int *>(base);
     Request *kept = reinterpret_cast<Request *>(base + ((kMaxRequests + 4) & ~3) * sizeof(int));
-    auto fact = [&](int r) { return r < kKept ? kept[r] : request(p, r); };
+    auto fact = [&](int r) { return r < kKept ? kept[r] : request<SHARED>(p, prefix, r); };
     {
         int run = 0;
         int *warp_sum = reinterpret_cast<int *>(s.sums);
@@ -241,7 +270,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             const int r = at + tid;
             int n = 0;
             if (r < p.n_req) {
-                const Request q = request(p, r);
+                const Request q = request<SHARED>(p, prefix, r);
                 n = q.items;
                 if (r < kKept)
                     kept[r] = q;
@@ -297,6 +326,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                         s.r = r;
                         s.m = m;
                         s.off = (int)(from - at);
+                        s.index = i;
                         s.first[0] = q.first;
                         s.first[1] = q.nq;
                         s.first[2] = q.before;
@@ -328,8 +358,12 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 here = blockIdx.x < g && from >= first && from < first + mine;
             }
         }
-        if (tid == 0)
+        if (tid == 0) {
             s.total = total;
+            if constexpr (SHARED)
+                if (blockIdx.x == 0)
+                    *prefix.n_items = run;
+        }
     }
     // TMA copies and the tensor core take over the space that these sums were in
     fence_async_smem();
@@ -344,7 +378,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------ exponentials and output
-        if (tid == 0)
+        if (!SHARED && tid == 0)
             plan.joins[2 * c] = plan.joins[2 * c + 1] = make_int4(0, 0, 0, 0);
         const uint32_t my_lanes = tmem + ((uint32_t)(warp * 32) << 16);
         // S: this thread has columns 8 g + 2 (lane % 4) + {0, 1} of rows r0 (x[4g], x[4g + 1]) and r0 + 8
@@ -353,7 +387,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         int tile = 0;                             // tiles of the block so far
         int flagged = 0;                          // of them, those whose rows were looked through
         long long unit = from;
-        Walk<R> w(p, s, units);
+        Walk<SHARED, R> w(p, prefix, s, units);
         while (ok) {
             const long long left = w.left;
             if (!w.next())
@@ -553,7 +587,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
             if (!ok)
                 break;
             // ---- output: whole items are finished here, parts go to the workspace
-            const bool done = w.t0 == 0 && w.t1 == w.nt;
+            const bool done = !SHARED && w.t0 == 0 && w.t1 == w.nt;
             if (w.t1 > w.t0) {
                 const int pt = tile - 1;
                 ok = mbar_wait(smem_addr(&s.kv_empty[pt % stages]), (pt / stages) & 1, status);
@@ -601,7 +635,17 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                     }
                 }
             } else {
-                const int64_t slot = 2 * (int64_t)c + (w.t0 == 0 ? 1 : 0);
+                // (SHARED: of the pairs (item, block) in the order of the units, each has at least one number of the two one higher)
+                const int64_t slot = SHARED ? (int64_t)w.index + c : 2 * (int64_t)c + (w.t0 == 0 ? 1 : 0);
+                if constexpr (SHARED) {
+                    if (tid == 0 && w.t0 == 0) {
+                        const int2 own = own_of(prefix, w.r);
+                        const int parts = w.nt == 0 ? 0 : holder(unit - 1 + (w.nt - w.t1), total, g) - c + 1;
+                        prefix.items[w.index] = OwnItem{(int)out_row, item_rows, own.x > 0 ? own.y : -1, parts, (int)slot};
+                    }
+                    if (w.t1 == w.t0)
+                        continue;
+                }
                 if ((lane & 3) == 0) {
                     plan.part_ml[slot * kTile + r0] = make_float2(m0, l0);
                     plan.part_ml[slot * kTile + r0 + 8] = make_float2(m1, l1);
@@ -620,7 +664,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                             *reinterpret_cast<float2 *>(dst + 8 * p.v_dim + n + 2 * i) = make_float2(o[i + 2], o[i + 3]);
                     }
                 }
-                if (tid == 0 && (w.t0 == 0 || plan.helpers)) {
+                if (!SHARED && tid == 0 && (w.t0 == 0 || plan.helpers)) {
                     // the blocks of the item's first and last tile: its units around the segment's last one
                     const int first = w.t0 == 0 ? c : holder(unit - w.t1, total, g);
                     plan.joins[slot] = make_int4((int)out_row, item_rows, first, holder(unit - 1 + (w.nt - w.t1), total, g));
@@ -675,7 +719,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         // tile's rows may wait for the product that frees their space), the product of the two: 250 against 248 us for
         // 608 tokens over 2048 rows of 512 columns, 335 against 305 us for rows of 576.
         int segment = 0, i = 0, i_st = 0, i_ph = 0, j = 0, j_st = 0;
-        Walk<R> w(p, s, units);
+        Walk<SHARED, R> w(p, prefix, s, units);
         while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
             const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
             if (n <= 0)
@@ -733,7 +777,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         const int lw = warp - (ROWS == kTma ? kTmaWarp : kMmaWarp) - 1;
         const uint8_t *cache = static_cast<const uint8_t *>(p.cache);
         int tile = 0, segment = 0;
-        Walk<R> w(p, s, units);
+        Walk<SHARED, R> w(p, prefix, s, units);
         while (ok && w.next()) {
             if (w.t1 <= w.t0)
                 continue;
@@ -778,7 +822,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
                 // page of one row (lane % 8) a turn ahead; 8-bit rows are fetched a turn ahead too (twice the registers
                 // would not do for bf16 rows).
                 const int end = visible(p, w.q, last_token(p, w.q, w.item()));
-                const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+                const int32_t *table = w.table();
                 const int n_groups = (w.t1 - w.t0) * kGroups;
                 constexpr bool kAhead = ROWS == kBits8;
                 constexpr int kParts = ROWS == kBits8 ? 1 : 2;  // 8-bit: lane / 4 is the row, else lane / 8 and + 4
@@ -875,10 +919,10 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const __grid_constant_
         const int copies = kGroups / plan.box_groups;
         uint32_t dirty = 0;  // stages whose flags are not all clear
         int tile = 0;
-        Walk<R> w(p, s, units);
+        Walk<SHARED, R> w(p, prefix, s, units);
         while (ok && w.next()) {
             const int end = visible(p, w.q, last_token(p, w.q, w.item()));
-            const int32_t *table = p.block_table + (int64_t)w.r * p.table_stride;
+            const int32_t *table = w.table();
             // lane % 8 finds the page of one of a tile's groups, a tile ahead
             auto needed = [&](int t) { return t < w.t1 && (lane & 7) < kGroups && t * R + (lane & 7) * 8 < end; };
             auto look_up = [&](int t) { return needed(t) ? load_now(table + p.by_page.quotient(t * R + (lane & 7) * 8)) : 0; };
@@ -1012,10 +1056,10 @@ template <bool HELPERS> __global__ void __launch_bounds__(128) latent_join_kerne
         p.lse[out_row] = tot == 0.0f ? -INFINITY : (ref + log2f(tot)) * kLn2;
 }
 
-template <Rows ROWS, int NK, int R>
-cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaStream_t st)
+template <bool SHARED, Rows ROWS, int NK, int R>
+cudaError_t go(const AttnParams &p, const MmaPlan &plan, const Prefix<SHARED> &prefix, unsigned *status, cudaStream_t st)
 {
-    auto kern = latent_mma_kernel<ROWS, NK, R>;
+    auto kern = latent_mma_kernel<SHARED, ROWS, NK, R>;
     cudaError_t e = allow_max_smem(reinterpret_cast<const void *>(kern));
     CUtensorMap boxes = {}, groups = {};
     if (ROWS == kTma && e == cudaSuccess && p.width > 0) {
@@ -1034,8 +1078,8 @@ cudaError_t go(const AttnParams &p, const MmaPlan &plan, unsigned *status, cudaS
     cfg.gridDim = dim3(plan.blocks);
     cfg.blockDim = dim3(kThreadsOf<ROWS, NK>);
     cfg.dynamicSmemBytes = plan.smem;
-    e = cudaLaunchKernelEx(&cfg, kern, p, plan, boxes, groups, status);
-    if (e != cudaSuccess)
+    e = cudaLaunchKernelEx(&cfg, kern, p, plan, prefix, boxes, groups, status);
+    if (e != cudaSuccess || SHARED)
         return e;
     cfg.gridDim = dim3((plan.helpers ? 2 : 1) * plan.blocks, kTile / 4);
     cfg.blockDim = dim3(128);
@@ -1087,17 +1131,50 @@ MmaPlan make_plan(const AttnParams &p, int num_sms)
     return m;
 }
 
-template <int NK> cudaError_t go_rows(const AttnParams &p, const MmaPlan &m, unsigned *status, cudaStream_t st)
+template <bool SHARED, int NK>
+cudaError_t go_rows(const AttnParams &p, const MmaPlan &m, const Prefix<SHARED> &prefix, unsigned *status, cudaStream_t st)
 {
     switch (rows_how(p)) {
-    case kTma: return go<kTma, NK, rows_of(kTma, NK)>(p, m, status, st);
-    case kRegisters: return go<kRegisters, NK, rows_of(kRegisters, NK)>(p, m, status, st);
-    default: return go<kBits8, NK, rows_of(kBits8, NK)>(p, m, status, st);
+    case kTma: return go<SHARED, kTma, NK, rows_of(kTma, NK)>(p, m, prefix, status, st);
+    case kRegisters: return go<SHARED, kRegisters, NK, rows_of(kRegisters, NK)>(p, m, prefix, status, st);
+    default: return go<SHARED, kBits8, NK, rows_of(kBits8, NK)>(p, m, prefix, status, st);
+    }
+}
+
+// LEAST: the narrowest rows that there are kernels for, in units of 64 columns.
+template <bool SHARED, int LEAST>
+cudaError_t launch_mma(const AttnParams &p, const Prefix<SHARED> &prefix, void *workspace, int num_sms, unsigned *status, cudaStream_t st)
+{
+    MmaPlan m = make_plan(p, num_sms);
+    if constexpr (SHARED) {
+        m.part_o = prefix.own_o;
+        m.part_ml = prefix.own_ml;
+    } else {
+        m.part_o = static_cast<float *>(workspace);
+        m.part_ml = reinterpret_cast<float2 *>(m.part_o + (size_t)m.blocks * 2 * kTile * p.v_dim);
+        m.joins = reinterpret_cast<int4 *>(m.part_ml + (size_t)m.blocks * 2 * kTile);
+    }
+    switch (p.head_dim / 64) {
+    case 1:
+        if constexpr (LEAST <= 1)
+            return go_rows<SHARED, 1>(p, m, prefix, status, st);
+        return cudaErrorInvalidValue;
+    case 2: return go_rows<SHARED, 2>(p, m, prefix, status, st);
+    case 3: return go_rows<SHARED, 3>(p, m, prefix, status, st);
+    case 4: return go_rows<SHARED, 4>(p, m, prefix, status, st);
+    case 5: return go_rows<SHARED, 5>(p, m, prefix, status, st);
+    case 6: return go_rows<SHARED, 6>(p, m, prefix, status, st);
+    case 7: return go_rows<SHARED, 7>(p, m, prefix, status, st);
+    case 8: return go_rows<SHARED, 8>(p, m, prefix, status, st);
+    case 9: return go_rows<SHARED, 9>(p, m, prefix, status, st);
+    default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
+// csa_latent_behind.cu compiles this file again for requests behind a prefix.
+#ifndef CSA_BEHIND_PREFIX
 bool latent_mma_supported(const AttnParams &p)
 {
     return p.head_dim % 64 == 0 && p.head_dim <= 576 && p.v_dim % 64 == 0 && p.v_dim <= 512;
@@ -1111,22 +1188,8 @@ size_t latent_mma_workspace(const AttnParams &p, int num_sms)
 
 cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms, unsigned *status, cudaStream_t st)
 {
-    MmaPlan m = make_plan(p, num_sms);
-    m.part_o = static_cast<float *>(workspace);
-    m.part_ml = reinterpret_cast<float2 *>(m.part_o + (size_t)m.blocks * 2 * kTile * p.v_dim);
-    m.joins = reinterpret_cast<int4 *>(m.part_ml + (size_t)m.blocks * 2 * kTile);
-    switch (p.head_dim / 64) {
-    case 1: return go_rows<1>(p, m, status, st);
-    case 2: return go_rows<2>(p, m, status, st);
-    case 3: return go_rows<3>(p, m, status, st);
-    case 4: return go_rows<4>(p, m, status, st);
-    case 5: return go_rows<5>(p, m, status, st);
-    case 6: return go_rows<6>(p, m, status, st);
-    case 7: return go_rows<7>(p, m, status, st);
-    case 8: return go_rows<8>(p, m, status, st);
-    case 9: return go_rows<9>(p, m, status, st);
-    default: return cudaErrorInvalidValue;
-    }
+    return launch_mma<false, 1>(p, NoPrefix{}, workspace, num_sms, status, st);
 }
+#endif
 
 }  // namespace csa

@@ -140,8 +140,10 @@ cudaError_t make_tensor_map_2d(CUtensorMap *m, const void *ptr, int64_t C, int b
 cudaError_t make_tensor_map_3d(CUtensorMap *m, const void *ptr, int64_t C, int chunk_cols, int chunks, int box_rows);
 // A [rows, 64 chunks] bf16 matrix with the given row stride (elements, rows a multiple of 8) seen as [rows / 8]
 // [chunks][8][64]: a box of `groups` groups of eight rows at (0, 0, 0, row / 8) lands, 128-byte swizzled, group by
-// group, in a group chunk by chunk.  Groups past the end read as zeros.
-cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups);
+// group, in a group chunk by chunk (box_chunks of them, from the third coordinate on; 0: all).  Groups and chunks past the end
+// read as zeros.
+cudaError_t make_tensor_map_groups(CUtensorMap *m, const void *ptr, int64_t rows, int chunks, int64_t stride, int groups,
+                                   int box_chunks = 0);
 cudaError_t make_tensor_map_parts(CUtensorMap *m, const void *ptr, int64_t C, int box_cols, int ratio, int head_dim);
 
 // The backward's kernel family and plan for one shape on the current device: one

@@ -330,7 +330,18 @@ int csa_shared_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     CSA_TRY(check_attention(q, q_token_stride, q_head_stride, cu_q, n_req, n_tokens, n_heads, head_dim, v_dim, cache, cache_stride,
                             cache_dtype, row_scales, n_pages, page_size, block_table, table_stride, width, seq_lens, ratio, scale,
                             sink, out, lse, &p, &some));
-    return some ? run_attention(p, stream) : CSA_OK;
+    if (!some)
+        return CSA_OK;
+    int sms = 0;
+    cudaMemPool_t pool = nullptr;
+    unsigned *status = nullptr;
+    cudaError_t e = csa::device_facts(&sms, &pool, &status);
+    if (e != cudaSuccess)
+        return cuda_status(e, "device set-up");
+    if (!csa::shared_mma_supported(p, n_groups, sms))
+        return run_attention(p, stream);
+    e = csa::launch_shared_mma(p, cu_groups, shared_rows, n_groups, sms, pool, status, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CSA_OK : cuda_status(e, "shared attention launch");
 }
 
 int csa_layer_norm_fwd(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, const float *weight,

@@ -154,6 +154,13 @@ struct AttnParams {
 bool latent_mma_supported(const AttnParams &p);
 size_t latent_mma_workspace(const AttnParams &p, int num_sms);
 cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms, unsigned *status, cudaStream_t st);
+// The same for groups of requests that share a prefix (csa_shared.cu); takes its workspace from the pool itself.
+bool shared_mma_supported(const AttnParams &p, int n_groups, int num_sms);
+cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, const int32_t *shared_rows, int n_groups, int num_sms,
+                              cudaMemPool_t pool, unsigned *status, cudaStream_t st);
+struct SharedPlan;
+int latent_behind_slots(const AttnParams &p, int num_sms);
+cudaError_t launch_latent_behind(const AttnParams &p, const SharedPlan &s, int num_sms, unsigned *status, cudaStream_t st);
 // Every other width.
 cudaError_t launch_attention_plain(const AttnParams &p, cudaStream_t st);
 

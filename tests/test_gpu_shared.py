@@ -12,9 +12,13 @@ import sparse_attention_kv_csa_gb300 as csa
 pytestmark = pytest.mark.gpu
 
 
-def made(groups, heads, dim, ratio, page, bits8=False, sink=False, seed=0, q_scale=1.0, spare=2, copies=False, width=0):
+def made(groups, heads, dim, ratio, page, bits8=False, sink=False, seed=0, q_scale=1.0, spare=2, copies=False, width=None):
     """groups: a list of (shared rows, [(rows behind them, new tokens), ...]).  The shared rows' whole pages are in every table
-    of the group; with copies each request has pages of its own with equal contents."""
+    of the group; with copies each request has pages of its own with equal contents.  A table with room for 160000 rows, which
+    these lengths do not use, makes the call worth the kernels for prefixes; one of just the pages in use (width 0) leaves most of
+    these small calls to the attention by requests."""
+    if width is None:
+        width = 160000 // page + 1
     g = torch.Generator().manual_seed(seed)
     rng = random.Random(seed)
     lens, news, cu_groups, need = [], [], [0], 0
@@ -95,10 +99,11 @@ TWO = [(520, [(30, 1), (61, 1), (16, 2)]), (130, [(3, 1), (300, 1), (12, 1), (9,
                                        (384, 384), (448, 256), (96, 96), (640, 640), (576, 576), (264, 8)])
 @pytest.mark.parametrize("bits8", [False, True])
 @pytest.mark.parametrize("sink", [False, True])
-def test_widths(dim, v_dim, bits8, sink):
+@pytest.mark.parametrize("width", [0, None])
+def test_widths(dim, v_dim, bits8, sink, width):
     if bits8 and dim % 16:
         pytest.skip("8-bit rows are multiples of 16 bytes")
-    check(made(TWO, 24, dim, 3, 16, bits8, sink, seed=dim), v_dim)
+    check(made(TWO, 24, dim, 3, 16, bits8, sink, seed=dim, width=width), v_dim)
 
 
 @pytest.mark.parametrize("heads", [1, 3, 16, 24, 63, 64, 65, 128, 130])
@@ -166,10 +171,14 @@ def test_narrow_tables_and_bad_entries():
     check(bad)
     narrow = dict(a, block_table=a["block_table"][:, :20].contiguous())  # 320 rows at most
     check(narrow)
-    wide = torch.full((3, 90), -1, dtype=torch.int32, device="cuda")
+    wide = torch.full((3, 12000), -1, dtype=torch.int32, device="cuda")
     wide[:, :a["block_table"].shape[1]] = a["block_table"]
-    strided = dict(a, block_table=wide[:, :40])
-    check(strided)
+    check(dict(a, block_table=wide[:, :11000]))
+    check(dict(a, block_table=wide[:, :40]))
+    # tables narrower than the rows, with enough requests for the prefix's kernels
+    a = made([(400, [(100 + k % 7, 1) for k in range(500)]), (300, [(k % 9, 1) for k in range(20)])], 16, 128, 1, 16, seed=21, width=0)
+    check(a)
+    check(dict(a, block_table=a["block_table"][:, :31].contiguous()))
 
 
 @pytest.mark.parametrize("bits8", [False, True])
@@ -292,6 +301,7 @@ def test_streams_and_two_graphs(bits8):
     # lengths and groups are read on the device: a replay follows them
     a["seq_lens"] -= 30
     a["shared_rows"] -= 64
+    a["cu_groups"][0] += 1
     graphs[0].replay()
     torch.cuda.synchronize()
     check(a, None, *results[0])
