@@ -112,7 +112,7 @@ template <bool SHARED> using Prefix = typename PrefixOf<SHARED>::type;
 
 // The rows of request r that its group's prefix part has (whole pages), and the group.
 __device__ __forceinline__ int2 own_of(const NoPrefix &, int) { return make_int2(0, -1); }
-__device__ __forceinline__ int2 own_of(const SharedPlan &s, int r) { return s.own[r]; }
+__device__ __forceinline__ int2 own_of(const SharedPlan &s, int r) { return __ldcg(s.own + r); }
 
 template <bool SHARED> __device__ __forceinline__ Request request(const AttnParams &p, const Prefix<SHARED> &prefix, int r)
 {
@@ -253,7 +253,10 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> p
         mbar_init(smem_addr(&s.drained), 1);
         mbar_init_fence();
     }
-    pdl_wait();
+    // SHARED: what this kernel reads was there before the one in front of it (the prefixes') let this one begin, so its blocks
+    // begin as that one's end, and wait for its end at their own.
+    if constexpr (!SHARED)
+        pdl_wait();
     pdl_trigger();
     if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&s.tmem), plan.tmem_columns);
@@ -650,8 +653,18 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> p
                     plan.part_ml[slot * kTile + r0] = make_float2(m0, l0);
                     plan.part_ml[slot * kTile + r0 + 8] = make_float2(m1, l1);
                 }
+                if constexpr (SHARED)
+                    for (int n = 0; n < p.v_dim; n += 64) {
+                        float o[32];
+                        tmem_ld_16x256(my_lanes + n, o);
+                        tmem_ld_16x256(my_lanes + n + 32, o + 16);
+                        tmem_wait_ld();
+                        float *dst = plan.part_o + (slot * kTile + r0) * p.v_dim + n;
+                        store_rows_16x256(dst, 8 * p.v_dim, o, live0, live1);
+                        store_rows_16x256(dst + 32, 8 * p.v_dim, o + 16, live0, live1);
+                    }
                 float *dst = plan.part_o + (slot * kTile + r0) * p.v_dim + cq;
-                for (int n = 0; n < p.v_dim; n += 64) {
+                for (int n = 0; !SHARED && n < p.v_dim; n += 64) {
                     float o[32];
                     tmem_ld_16x256(my_lanes + n, o);
                     tmem_ld_16x256(my_lanes + n + 32, o + 16);
@@ -968,6 +981,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> p
         tc_fence_after();
         tmem_free(tmem, plan.tmem_columns);
     }
+    if constexpr (SHARED)
+        pdl_wait();
 }
 
 // Joins the parts of the items that cross block boundaries, a warp a row.  Part k of n is slot 1 of the item's first block

@@ -320,21 +320,14 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
             if (tid < kHalf)
                 s.part_ml[slot + row] =
                     make_float2(m, (sh.exchange[row] + sh.exchange[row + 64]) + (sh.exchange[row + 128] + sh.exchange[row + 192]));
-#pragma unroll 1
             for (int sub = 0; sub < 2; ++sub) {
                 const int r = (warp & 1) * 32 + sub * 16 + lane / 4, left = rows - (int)rank * kHalf;
-                float *dst = s.part_o + (slot + r) * p.v_dim + half * v_half + 2 * (lane & 3);
+                float *dst = s.part_o + (slot + r) * p.v_dim + half * v_half;
                 for (int n = part * 32; n < v_half; n += 64) {
                     float o[16];
                     tmem_ld_16x256(my_lanes + ((uint32_t)(sub * 16) << 16) + n, o);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        if (r < left)
-                            *reinterpret_cast<float2 *>(dst + n + 2 * i) = make_float2(o[i], o[i + 1]);
-                        if (r + 8 < left)
-                            *reinterpret_cast<float2 *>(dst + 8 * p.v_dim + n + 2 * i) = make_float2(o[i + 2], o[i + 3]);
-                    }
+                    store_rows_16x256(dst + n, 8 * p.v_dim, o, r < left, r + 8 < left);
                 }
             }
             tc_fence_before();
@@ -558,6 +551,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                 if (row < rows)
                     src += ((int64_t)token * p.q_token_stride + (int64_t)(flat - token * (uint32_t)p.n_heads) * p.q_head_stride) * 2;
                 const uint32_t dst = smem_addr(q_mem) + row * 128 + ((unit ^ (row & 7)) << 4);
+#pragma unroll 4
                 for (int ch = 0; ch < nk; ++ch)
                     copy_async_16(dst + ch * kQueryChunk, src + ch * 128, row < rows);
             }

@@ -268,6 +268,35 @@ __device__ __forceinline__ void tmem_st_32x32(uint32_t taddr, const float *v)
                  : "memory");
 }
 
+// Writes what tmem_ld_16x256 gave to rows of fp32: row lane / 4 at `dst` (32 columns on a 128-byte boundary) and the eighth one behind
+// it `eight` floats on.  The four threads of a row exchange so that each has eight columns in a row: whole lines with one
+// store (64 rows x 512 columns of a block 5200 cycles, pairs of columns 6100; the rest is L2's, 7 TB/s when all blocks write).
+__device__ __forceinline__ void store_rows_16x256(float *dst, int64_t eight, const float *o, bool first, bool second)
+{
+    const int q = threadIdx.x & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float2 v[4];  // columns 8 g + 2 q + {0, 1}
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            v[g] = make_float2(o[4 * g + 2 * h], o[4 * g + 2 * h + 1]);
+        auto swap = [&](float2 &a, float2 &b, int x) {
+            const float2 s = (q & x) ? a : b;
+            const float2 r = make_float2(__shfl_xor_sync(~0u, s.x, x), __shfl_xor_sync(~0u, s.y, x));
+            a = (q & x) ? r : a;
+            b = (q & x) ? b : r;
+        };
+        swap(v[0], v[1], 1);
+        swap(v[2], v[3], 1);
+        swap(v[0], v[2], 2);
+        swap(v[1], v[3], 2);  // columns 8 q + 2 g + {0, 1}
+        if (h ? second : first)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + h * eight + 8 * q), "f"(v[0].x), "f"(v[0].y),
+                         "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+                         : "memory");
+    }
+}
+
 // Sixteen bytes from global to shared memory without a register in between (zeros unless `some`), and the wait for all of the
 // thread's.
 __device__ __forceinline__ void copy_async_16(uint32_t dst, const void *src, bool some)
