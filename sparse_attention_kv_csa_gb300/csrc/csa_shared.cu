@@ -43,6 +43,7 @@ constexpr int kQueryChunk = kHalf * 128;  // bytes of 64 columns of a block's qu
 constexpr int kSoftWarps = 8, kScoreWarp = 8, kValueWarp = 9, kCopyWarp = 10, kCopyWarps = 4, kQueryWarp = 14, kQueryWarps = 2;
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kMaxSlots = 16;
+constexpr int kBatch = 2;  // units that an MMA warp waits for at once
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;  // log2 of how far a logit may exceed the reference
@@ -52,7 +53,7 @@ struct PairPlan {
     int nk;           // chunks of 64 columns of a row
     int vch;          // chunks of a block's half of the value columns
     int cw;           // chunks of a unit
-    int slots;        // units in the ring
+    int k_slots, v_slots;  // units in the rings of K and V
     int box_groups;   // groups of eight rows of the larger copy
     size_t smem;
 };
@@ -118,14 +119,14 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
     __shared__ PairShared sh;
     uint8_t *mem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     constexpr int cw = CW, group_bytes = cw * 1024, unit_bytes = 8 * group_bytes;
-    const int nk = plan.nk, slots = plan.slots;
+    const int nk = plan.nk;
     uint8_t *q_mem = mem, *p_mem = q_mem + nk * kQueryChunk, *kv_mem = p_mem + 4 * kQueryChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int c = blockIdx.x / 2;
 
     if (tid == 0) {
-        for (int i = 0; i < slots; ++i) {
+        for (int i = 0; i < plan.k_slots + plan.v_slots; ++i) {
             mbar_init(smem_addr(&sh.kv_full[i]), 1);
             mbar_init(smem_addr(&sh.kv_empty[i]), 1);
         }
@@ -335,28 +336,41 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
     } else if (warp <= kValueWarp) {
         // ------------------------------------------------ matrix products, issued by the even block
         // Two warps, one for S and one for O: between its products each spends as long again on waits and loops, while the other's
-        // run (one warp for both: 3050 cycles a tile).  Units are taken in twos for the same reason.  The ring holds, in this
-        // order, the units of K of tile 0, of K of 1 and V of 0, of K of 2 and V of 1, ...
+        // run (one warp for both: 3050 cycles a tile).  Units are taken kBatch at a time for the same reason.  Each has a ring of its
+        // own: a barrier's parity says that a phase is over only to who knows that the one before is, as a ring's only reader does.
         if (rank == 0) {
             const uint32_t tm = __shfl_sync(~0u, tmem, 0);
             const uint64_t q_desc = mma_operand(smem_addr(q_mem), 16, 1024), p_desc = mma_operand(smem_addr(p_mem), 16, 1024);
             const uint64_t k_desc = mma_operand(smem_addr(kv_mem), 16, group_bytes), v_desc = mma_operand(smem_addr(kv_mem), 1024, group_bytes);
             constexpr uint32_t unit_step = unit_bytes >> 4, sixteen = 2 * group_bytes >> 4;
             constexpr uint32_t kQueryStep = kQueryChunk >> 4, kChunkStep = 1024 >> 4;
-            const int k_units = (nk + cw - 1) / cw, v_units = 2 * ((plan.vch + cw - 1) / cw);
+            const int base = warp == kScoreWarp ? 0 : plan.k_slots, slots = warp == kScoreWarp ? plan.k_slots : plan.v_slots;
             struct Place {
                 int slot;
                 uint32_t ph;
             };
-            auto move = [&](Place a, int units) {
-                for (a.slot += units; a.slot >= slots; a.slot -= slots)
-                    a.ph ^= 1;
-                return a;
-            };
+            auto behind = [&](Place a) { return a.slot + 1 == base + slots ? Place{base, a.ph ^ 1} : Place{a.slot + 1, a.ph}; };
             auto ready = [&](Place a) { return mbar_test_cluster(smem_addr(&sh.kv_full[a.slot]), a.ph); };
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait_cluster(smem_addr(bar), parity, status)); };
-            Place at{0, 0};
+            Place at{base, 0};
             int tile = 0;
+            // the next units, all there or the wait gave up
+            auto arrived = [&](Place (&u)[kBatch], int count) {
+                bool here = true;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    u[i] = at;
+                    if (i < count) {
+                        here &= ready(at);
+                        at = behind(at);
+                    }
+                }
+                if (!__all_sync(~0u, here))
+                    for (int i = 0; i < count && ok; ++i)
+                        wait(&sh.kv_full[u[i].slot], u[i].ph);
+                tc_fence_after();
+                return ok;
+            };
             PairWalk w(s, sh, units);
             if (warp == kScoreWarp) {
                 constexpr uint32_t shape_s = mma_shape(kPairRows, kPairRows, false);
@@ -368,85 +382,68 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                         if (tile > 1)
                             wait(&sh.p_full[tile & 1], (tile - 2) >> 1 & 1);  // S of two tiles before has been read
                         const uint32_t d = tm + 256 + (tile & 1) * 64;
-                        for (int first = 0; ok && first < nk; first += 2 * cw) {
-                            const bool two = first + cw < nk, last = first + 2 * cw >= nk;
-                            const Place a = at, b = move(a, 1);
-                            bool here = ready(a);
-                            if (two)
-                                here &= ready(b);
-                            if (!__all_sync(~0u, here)) {
-                                wait(&sh.kv_full[a.slot], a.ph);
-                                if (ok && two)
-                                    wait(&sh.kv_full[b.slot], b.ph);
-                                if (!ok)
-                                    break;
-                            }
-                            tc_fence_after();
+                        for (int first = 0; ok && first < nk; first += kBatch * cw) {
+                            const int count = min(kBatch, (nk - first + cw - 1) / cw);
+                            Place u[kBatch];
+                            if (!arrived(u, count))
+                                break;
                             if (elect_one()) {
                                 const uint64_t q = q_desc + (uint32_t)first * kQueryStep;
-                                const uint64_t k[2] = {k_desc + (uint32_t)a.slot * unit_step, k_desc + (uint32_t)b.slot * unit_step};
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
+                                for (int i = 0; i < kBatch; ++i)
+                                    if (i < count) {
+                                        const uint64_t k = k_desc + (uint32_t)u[i].slot * unit_step;
 #pragma unroll
-                                    for (int ch = 0; ch < CW; ++ch)
-                                        if (first + u * CW + ch < nk)
+                                        for (int ch = 0; ch < CW; ++ch)
+                                            if (first + i * CW + ch < nk)
 #pragma unroll
-                                            for (int i = 0; i < 4; ++i)
-                                                mma_bf16_pair(d, q + (u * CW + ch) * kQueryStep + i * 2, k[u] + ch * kChunkStep + i * 2, shape_s,
-                                                              u > 0 || ch > 0 || i > 0 || first > 0);
-                                    if (u == 0 || two)
-                                        mma_commit_pair(smem_addr(&sh.kv_empty[u ? b.slot : a.slot]));
-                                }
-                                if (last)
+                                                for (int x = 0; x < 4; ++x)
+                                                    mma_bf16_pair(d, q + (i * CW + ch) * kQueryStep + x * 2, k + ch * kChunkStep + x * 2, shape_s,
+                                                                  i > 0 || ch > 0 || x > 0 || first > 0);
+                                        mma_commit_pair(smem_addr(&sh.kv_empty[u[i].slot]));
+                                    }
+                                if (first + kBatch * cw >= nk) {
                                     mma_commit_pair(smem_addr(&sh.s_full[tile & 1]));
-                                if (last && j + 1 == n)
-                                    mma_commit_pair(smem_addr(&sh.q_empty));
+                                    if (j + 1 == n)
+                                        mma_commit_pair(smem_addr(&sh.q_empty));
+                                }
                             }
                             __syncwarp();
-                            at = two ? move(b, 1) : b;
                         }
-                        at = move(at, (j > 0 ? v_units : 0) + (j + 1 == n ? v_units : 0));
                     }
                 }
             } else {
                 while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
                     const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
-                    at = move(at, k_units);
                     for (int j = 0; ok && j < n; ++j, ++tile) {  // O (+)= P V
-                        if (j + 1 < n)
-                            at = move(at, k_units);
-                        for (int col = 0; ok && col < v_half; col += cw * 64) {
-                            const Place a = at, b = move(a, 1);
-                            bool here = ready(a);
-                            here &= ready(b);
-                            if (col == 0)
-                                here &= mbar_test_cluster(smem_addr(&sh.p_full[tile & 1]), tile >> 1 & 1);
-                            if (!__all_sync(~0u, here)) {
-                                wait(&sh.kv_full[a.slot], a.ph);
-                                if (ok)
-                                    wait(&sh.kv_full[b.slot], b.ph);
-                                if (ok && col == 0)
-                                    wait(&sh.p_full[tile & 1], tile >> 1 & 1);
+                        for (int col = 0; ok && col < v_half; col += kBatch / 2 * cw * 64) {
+                            const int count = min(kBatch, 2 * ((v_half - col + cw * 64 - 1) / (cw * 64)));
+                            Place u[kBatch];
+                            if (!arrived(u, count))
+                                break;
+                            if (col == 0) {
+                                wait(&sh.p_full[tile & 1], tile >> 1 & 1);
                                 if (!ok)
                                     break;
+                                tc_fence_after();
                             }
-                            tc_fence_after();
                             if (elect_one()) {
-                                const uint32_t shape = mma_shape(kPairRows, 2 * min(cw * 64, v_half - col), true);
                                 const uint64_t pa = p_desc + (uint32_t)((tile & 1) * 2) * kQueryStep;
-                                const uint64_t v[2] = {v_desc + (uint32_t)a.slot * unit_step, v_desc + (uint32_t)b.slot * unit_step};
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
+                                for (int i = 0; i < kBatch; ++i)
+                                    if (i < count) {
+                                        const int to = col + i / 2 * cw * 64;
+                                        const uint32_t shape = mma_shape(kPairRows, 2 * min(cw * 64, v_half - to), true);
+                                        const uint64_t v = v_desc + (uint32_t)u[i].slot * unit_step;
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        mma_bf16_pair(tm + col, pa + h * kQueryStep + k * 2, v[h] + k * sixteen, shape, h > 0 || k > 0 || j > 0);
-                                    mma_commit_pair(smem_addr(&sh.kv_empty[h ? b.slot : a.slot]));
-                                }
-                                if (col + cw * 64 >= v_half)
+                                        for (int k = 0; k < 4; ++k)
+                                            mma_bf16_pair(tm + to, pa + (i & 1) * kQueryStep + k * 2, v + k * sixteen, shape, (i & 1) > 0 || k > 0 || j > 0);
+                                        mma_commit_pair(smem_addr(&sh.kv_empty[u[i].slot]));
+                                    }
+                                if (col + kBatch / 2 * cw * 64 >= v_half)
                                     mma_commit_pair(smem_addr(&sh.pv_done[tile & 1]));
                             }
                             __syncwarp();
-                            at = move(b, 1);
                         }
                     }
                 }
@@ -460,13 +457,16 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
         }
     } else if (warp < kQueryWarp) {
         // ------------------------------------------------ rows by TMA, counted on the even block's barriers
-        // (warps in turn: one took some 450 cycles a unit, with eight units a tile of 2048 cycles)
+        // (two warps in turn for K, two for V: one took some 450 cycles a unit, with eight units a tile of 2048 cycles)
+        const bool values = warp >= kCopyWarp + kCopyWarps / 2;
+        const int base = values ? plan.k_slots : 0, slots = values ? plan.v_slots : plan.k_slots;
         const uint32_t kv_smem = smem_addr(kv_mem), full0 = at_rank(smem_addr(&sh.kv_full[0]), 0);
         const bool image = s.image_rows > 0;
         const int none = (int)(image ? (int64_t)s.n_groups * s.image_rows / 8 : p.n_pages * p.page_size / 8);  // a group past the end reads as zeros
         const int copies = 8 / plan.box_groups;
-        int slot = 0, filled = 0, turn = warp - kCopyWarp, last_filled = -1;
+        int slot = base, filled = 0, last_filled = -1;
         uint32_t ph = 0;
+        bool turn = (warp - kCopyWarp) % 2 == 0;
         PairWalk w(s, sh, units);
         while (ok && w.next()) {
             const int32_t *table = p.block_table + (int64_t)w.q.first * p.table_stride;
@@ -483,7 +483,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
             };
             // 64 rows from group `first` of the tile on, chunks from `chunk` on
             auto fill = [&](int at, bool whole, int first, int chunk) {
-                if (turn == 0 && ok) {
+                if (turn && ok) {
                     const int g = __shfl_sync(~0u, at, first + (whole ? lane * plan.box_groups : lane) % 8);
                     if (filled >= slots) {
                         ok = mbar_wait(smem_addr(&sh.kv_empty[slot]), ph ^ 1, status);
@@ -499,35 +499,32 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                         last_filled = filled;
                     }
                 }
-                turn = turn == 0 ? kCopyWarps - 1 : turn - 1;
+                turn = !turn;
                 ++filled;
-                if (++slot == slots) {
-                    slot = 0;
+                if (++slot == base + slots) {
+                    slot = base;
                     ph ^= 1;
                 }
             };
-            int now = look_up(w.t0), last = none;
-            bool last_whole = false;
-            for (int t = w.t0; ok && t <= w.t1; ++t) {
+            int now = look_up(w.t0);
+            for (int t = w.t0; ok && t < w.t1; ++t) {
                 const bool whole = image || (t + 1) * kPairRows <= w.q.shared;
                 const int next = look_up(t + 1);
-                if (t < w.t1)
+                if (values)
+                    for (int at = 0; at < plan.vch; at += cw) {
+                        fill(now, whole, 0, rank * plan.vch + at);
+                        fill(now, whole, 8, rank * plan.vch + at);
+                    }
+                else
                     for (int first = 0; first < nk; first += cw)
                         fill(now, whole, rank * 8, first);
-                if (t > w.t0)
-                    for (int at = 0; at < plan.vch; at += cw) {
-                        fill(last, last_whole, 0, rank * plan.vch + at);
-                        fill(last, last_whole, 8, rank * plan.vch + at);
-                    }
-                last = now;
-                last_whole = whole;
                 now = next;
             }
         }
         // no copy outlives the blocks, after a wait that gave up either (the even block's barriers count both blocks' copies)
         if (rank == 0 && lane == 0 && !ok)
-            for (int k = last_filled; k >= 0 && k > last_filled - slots; k -= kCopyWarps)
-                mbar_wait(smem_addr(&sh.kv_full[k % slots]), (k / slots) & 1, status);
+            for (int k = last_filled; k >= 0 && k > last_filled - slots; k -= 2)
+                mbar_wait(smem_addr(&sh.kv_full[base + k % slots]), (k / slots) & 1, status);
         __syncwarp();
     } else {
         // ------------------------------------------------ queries, by copies of sixteen bytes
@@ -767,9 +764,13 @@ PairPlan make_plan(const AttnParams &p)
     m.cw = m.vch < 2 ? m.vch : 2;
     const size_t unit = (size_t)m.cw * 8 * 1024, fixed = (size_t)(m.nk + 4) * kQueryChunk + 1024;
     const size_t limit = 227 * 1024 - sizeof(PairShared);
-    m.slots = (int)((limit - fixed) / unit);
-    m.slots = m.slots > kMaxSlots ? kMaxSlots : m.slots;
-    m.smem = fixed + m.slots * unit;
+    // the rings' sizes go as the units of a tile, and are two or more: an MMA warp waits for two units at once
+    const int fit = (int)((limit - fixed) / unit), slots = fit > kMaxSlots ? kMaxSlots : fit;
+    const int k_units = (m.nk + m.cw - 1) / m.cw, v_units = 2 * ((m.vch + m.cw - 1) / m.cw);
+    const int k_slots = (slots * k_units + (k_units + v_units) / 2) / (k_units + v_units);
+    m.k_slots = k_slots < kBatch ? kBatch : k_slots > slots - kBatch ? slots - kBatch : k_slots;
+    m.v_slots = slots - m.k_slots;
+    m.smem = fixed + slots * unit;
     // a block an SM, beside none of the attention's by requests, which own tensor memory too
     m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
     const int groups = needs_image(p) ? 8 : p.page_size / 8;
@@ -852,9 +853,12 @@ bool shared_mma_supported(const AttnParams &p, int n_groups, int num_sms)
 {
     if (!latent_mma_supported(p) || p.v_dim % 128 != 0 || n_groups < 1 || p.n_req < 2 || p.width * p.page_size < kLeastShared || (needs_image(p) && image_rows(p, n_groups) < kPairRows))
         return false;
-    // Little to share (at most some sixteen tiles an SM): the attention by requests has two launches to five here.
+    // By requests an SM does a tile of 64 query rows x 64 rows in some 1 us, here the prefix's in 0.6, behind some 25 us of launches, parts
+    // and their join.  Measured, in such tiles an SM by the table's width: 24 of 576 columns 59.5 us here, 54.8 by requests; another
+    // 24 45.8 and 49.6; 30 of 256 columns 38.5 and 39.6; with an image 31: 77.9 and 54.0, 70: 121 and 123.
+    const int64_t rows = p.n_tokens * p.n_heads / kOwnRows, items = rows > p.n_req ? rows : p.n_req;
     const int64_t tiles = ((int64_t)p.width * p.page_size + 63) / 64;
-    if (own_items(p) * tiles < 16 * (int64_t)num_sms)
+    if (items * tiles < (needs_image(p) ? 64 : 24) * (int64_t)num_sms)
         return false;
     // (the parts of a prompt's many tokens would take too much room: they fill the machine request by request)
     return ((p.n_tokens * p.n_heads / kPairRows + n_groups) * kPairRows + (int64_t)own_items(p) * kOwnRows) * p.v_dim * 4 <= (int64_t)1 << 32;

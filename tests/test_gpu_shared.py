@@ -14,11 +14,11 @@ pytestmark = pytest.mark.gpu
 
 def made(groups, heads, dim, ratio, page, bits8=False, sink=False, seed=0, q_scale=1.0, spare=2, copies=False, width=None):
     """groups: a list of (shared rows, [(rows behind them, new tokens), ...]).  The shared rows' whole pages are in every table
-    of the group; with copies each request has pages of its own with equal contents.  A table with room for 160000 rows, which
+    of the group; with copies each request has pages of its own with equal contents.  A table with room for 400000 rows, which
     these lengths do not use, makes the call worth the kernels for prefixes; one of just the pages in use (width 0) leaves most of
     these small calls to the attention by requests."""
     if width is None:
-        width = 160000 // page + 1
+        width = 400000 // page + 1
     g = torch.Generator().manual_seed(seed)
     rng = random.Random(seed)
     lens, news, cu_groups, need = [], [], [0], 0
@@ -171,12 +171,12 @@ def test_narrow_tables_and_bad_entries():
     check(bad)
     narrow = dict(a, block_table=a["block_table"][:, :20].contiguous())  # 320 rows at most
     check(narrow)
-    wide = torch.full((3, 12000), -1, dtype=torch.int32, device="cuda")
+    wide = torch.full((3, 27000), -1, dtype=torch.int32, device="cuda")
     wide[:, :a["block_table"].shape[1]] = a["block_table"]
-    check(dict(a, block_table=wide[:, :11000]))
+    check(dict(a, block_table=wide[:, :26000]))
     check(dict(a, block_table=wide[:, :40]))
     # tables narrower than the rows, with enough requests for the prefix's kernels
-    a = made([(400, [(100 + k % 7, 1) for k in range(500)]), (300, [(k % 9, 1) for k in range(20)])], 16, 128, 1, 16, seed=21, width=0)
+    a = made([(400, [(100 + k % 7, 1) for k in range(700)]), (300, [(k % 9, 1) for k in range(20)])], 16, 128, 1, 16, seed=21, width=0)
     check(a)
     check(dict(a, block_table=a["block_table"][:, :31].contiguous()))
 
