@@ -42,6 +42,9 @@ constexpr int kHead = 3;
 // rows: 26.9, 27.6 and 32.0.
 constexpr int kMinUnits = 3;
 
+// The same for an item of a shared prefix.
+constexpr int kPairHead = 2;
+
 #ifndef __CUDA_ARCH__
 using std::max;
 using std::min;

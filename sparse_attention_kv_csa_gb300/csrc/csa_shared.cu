@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(256) shared_plan_kernel(const AttnParams p, co
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ int fewest;
+    __shared__ int fewest, reader;  // reader: the first request with new tokens, whose table is read
     const int g = blockIdx.x, tid = threadIdx.x;
     auto bound = [&](int i) { return min(max(__ldg(cu_groups + i), 0), p.n_req); };
     const int r0 = bound(g), r1 = max(bound(g + 1), r0);
@@ -583,14 +583,17 @@ __global__ void __launch_bounds__(256) shared_plan_kernel(const AttnParams p, co
     int most = min(max(__ldg(shared_rows + g), 0), p.width * p.page_size);
     if (s.image_rows > 0)
         most = min(most, s.image_rows);
-    if (tid == 0)
+    if (tid == 0) {
         fewest = most;
+        reader = r1;
+    }
     __syncthreads();
     // Rows that every new token sees: the first one of each request sees the fewest.  (None where a request has more rows than
     // its table lists, so that the rows behind a prefix end with the table.)
     for (int r = r0 + tid; r < r1; r += 256) {
         const int at = __ldg(p.cu_q + r), end = __ldg(p.cu_q + r + 1);
         if (min((int64_t)end, p.n_tokens) > max(at, 0)) {
+            atomicMin(&reader, r);
             const int held = __ldg(p.seq_lens + r) - (end - at) + 1;
             const int all = max(__ldg(p.seq_lens + r), 0);
             const bool listed = (int)p.by_ratio.quotient((uint32_t)all) <= p.width * p.page_size;
@@ -598,14 +601,14 @@ __global__ void __launch_bounds__(256) shared_plan_kernel(const AttnParams p, co
         }
     }
     __syncthreads();
-    const int pages = (int)p.by_page.quotient((uint32_t)fewest);
+    const int pages = reader < r1 ? (int)p.by_page.quotient((uint32_t)fewest) : 0, first = reader;
     __syncthreads();
     if (tid == 0)
         fewest = pages;
     __syncthreads();
     // pages that lie in the cache, up to the first that does not
     for (int i = tid; i < pages; i += 256) {
-        const int page = __ldg(p.block_table + (int64_t)r0 * p.table_stride + i);
+        const int page = __ldg(p.block_table + (int64_t)first * p.table_stride + i);
         if (page < 0 || page >= p.n_pages)
             atomicMin(&fewest, i);
     }
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(256) shared_plan_kernel(const AttnParams p, co
     if (shared < least || r1 - r0 < 2 || rows == 0)
         shared = 0;
     if (tid == 0)
-        s.groups[g] = GroupInfo{shared, (shared + kPairRows - 1) / kPairRows, row0, rows, r0, shared ? (rows + kPairRows - 1) / kPairRows : 0};
+        s.groups[g] = GroupInfo{shared, (shared + kPairRows - 1) / kPairRows, row0, rows, first, shared ? (rows + kPairRows - 1) / kPairRows : 0};
     for (int r = r0 + tid; r < r1; r += 256)
         s.own[r] = make_int2(shared, g);
     // requests outside of all groups
@@ -771,8 +774,8 @@ PairPlan make_plan(const AttnParams &p)
     m.k_slots = k_slots < kBatch ? kBatch : k_slots > slots - kBatch ? slots - kBatch : k_slots;
     m.v_slots = slots - m.k_slots;
     m.smem = fixed + slots * unit;
-    // a block an SM, beside none of the attention's by requests, which own tensor memory too
-    m.smem = m.smem < 120 * 1024 ? 120 * 1024 : m.smem;
+    // a block an SM, beside none of the attention by requests (90 KB or more), which has tensor memory too
+    m.smem = m.smem < 140 * 1024 ? 140 * 1024 : m.smem;
     const int groups = needs_image(p) ? 8 : p.page_size / 8;
     for (m.box_groups = 8; groups % m.box_groups; m.box_groups /= 2) {}
     return m;

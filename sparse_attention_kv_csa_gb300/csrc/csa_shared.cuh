@@ -12,14 +12,12 @@
 namespace csa {
 
 constexpr int kPairRows = 128;  // query rows of an item, and cache rows of a tile
-// Units of an item besides its tiles, for its queries and output.
-constexpr int kPairHead = 2;
 
 struct GroupInfo {
     int shared;  // rows that the group's prefix part takes: whole pages, seen by every new token of the group
     int tiles;
     int row0, rows;  // its query rows: (token, head) pairs
-    int first;       // its first request, whose table lists the prefix
+    int first;       // its first request with new tokens, whose table lists the prefix
     int items;
 };
 

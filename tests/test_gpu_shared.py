@@ -307,6 +307,34 @@ def test_streams_and_two_graphs(bits8):
     check(a, None, *results[0])
 
 
+def test_finished_requests_in_front():
+    # the group's first requests have no new tokens and no pages any more
+    a = made([(700, [(0, 0), (0, 0), (30, 1), (64, 2), (5, 1)])], 64, 512, 1, 64, seed=22)
+    a["block_table"][:2] = -1
+    a["seq_lens"][:2] = 0
+    check(a)
+    # nobody has
+    b = dict(a, q=a["q"][:0], cu_q=torch.zeros_like(a["cu_q"]))
+    out, lse = csa.shared_attention(**b)
+    assert out.shape == (0, 64, 512)
+    b = dict(a, cu_q=torch.zeros_like(a["cu_q"]), out=torch.full_like(a["q"], 7.0))  # tokens of no request
+    assert (csa.shared_attention(**b)[0] == 7).all()
+
+
+def test_many_calls_at_once():
+    sets = [made([(600 + 64 * k, [(30 + k, 1)] * (3 + k))], 64, 512 if k % 2 else 576, 1, 64, k == 3, True, seed=30 + k) for k in range(4)]
+    want = [csa.shared_attention(**a, v_dim=512) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(6):
+        got += [(k, csa.shared_attention(**a, v_dim=512, stream=s)) for k, (a, s) in enumerate(zip(sets, streams))]
+    torch.cuda.synchronize()
+    assert csa.csa_device_status() == 0
+    for k, (out, lse) in got:
+        assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+
+
 def test_nothing_to_do():
     a = made(ONE, 16, 512, 1, 64, seed=19)
     out, lse = csa.shared_attention(**dict(a, q=a["q"][:0]))
