@@ -350,8 +350,8 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                 uint32_t ph;
             };
             auto behind = [&](Place a) { return a.slot + 1 == base + slots ? Place{base, a.ph ^ 1} : Place{a.slot + 1, a.ph}; };
-            auto ready = [&](Place a) { return mbar_test_cluster(smem_addr(&sh.kv_full[a.slot]), a.ph); };
-            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait_cluster(smem_addr(bar), parity, status)); };
+            auto ready = [&](Place a) { return mbar_test(smem_addr(&sh.kv_full[a.slot]), a.ph); };
+            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait(smem_addr(bar), parity, status)); };
             Place at{base, 0};
             int tile = 0;
             // the next units, all there or the wait gave up
@@ -413,15 +413,16 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                     }
                 }
             } else {
+                const int v_units = 2 * ((plan.vch + cw - 1) / cw);
                 while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
                     const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
                     for (int j = 0; ok && j < n; ++j, ++tile) {  // O (+)= P V
-                        for (int col = 0; ok && col < v_half; col += kBatch / 2 * cw * 64) {
-                            const int count = min(kBatch, 2 * ((v_half - col + cw * 64 - 1) / (cw * 64)));
+                        for (int first = 0; ok && first < v_units; first += kBatch) {
+                            const int count = min(kBatch, v_units - first);
                             Place u[kBatch];
                             if (!arrived(u, count))
                                 break;
-                            if (col == 0) {
+                            if (first == 0) {
                                 wait(&sh.p_full[tile & 1], tile >> 1 & 1);
                                 if (!ok)
                                     break;
@@ -432,15 +433,15 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
 #pragma unroll
                                 for (int i = 0; i < kBatch; ++i)
                                     if (i < count) {
-                                        const int to = col + i / 2 * cw * 64;
+                                        const int half = (first + i) & 1, to = (first + i) / 2 * cw * 64;
                                         const uint32_t shape = mma_shape(kPairRows, 2 * min(cw * 64, v_half - to), true);
                                         const uint64_t v = v_desc + (uint32_t)u[i].slot * unit_step;
 #pragma unroll
                                         for (int k = 0; k < 4; ++k)
-                                            mma_bf16_pair(tm + to, pa + (i & 1) * kQueryStep + k * 2, v + k * sixteen, shape, (i & 1) > 0 || k > 0 || j > 0);
+                                            mma_bf16_pair(tm + to, pa + half * kQueryStep + k * 2, v + k * sixteen, shape, half > 0 || k > 0 || j > 0);
                                         mma_commit_pair(smem_addr(&sh.kv_empty[u[i].slot]));
                                     }
-                                if (col + kBatch / 2 * cw * 64 >= v_half)
+                                if (first + kBatch >= v_units)
                                     mma_commit_pair(smem_addr(&sh.pv_done[tile & 1]));
                             }
                             __syncwarp();

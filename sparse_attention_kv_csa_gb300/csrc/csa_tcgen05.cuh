@@ -156,50 +156,10 @@ __device__ __forceinline__ void cluster_barrier()
 
 // An arrival at a barrier of either block.  What it orders are reads of tensor memory (behind tcgen05.fence) and writes to this
 // block's own shared memory (behind fence.proxy.async), for the products that read them here: nothing of global memory, for which
-// a release at the cluster's scope takes some 2000 cycles.
+// a release at the cluster's scope takes some 2000 cycles (and an acquire some 100 in the warps that issue the products).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// mbar_test and mbar_wait for a barrier at which threads of the other block arrive too.
-__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned *status)
-{
-    auto done = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        return ok != 0;
-    };
-    if (done())
-        return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t it = 1; it < (1u << 28); ++it) {
-        if (done())
-            return true;
-        if ((it & 255u) == 0 && global_ns() - t0 > kWaitLimitNs)
-            break;
-    }
-    atomicCAS(status, 0u, kStatusTimeout);
-    return false;
 }
 
 // (a warp of each block)
