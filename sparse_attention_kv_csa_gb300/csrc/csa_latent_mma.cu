@@ -365,7 +365,7 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> p
             s.total = total;
             if constexpr (SHARED)
                 if (blockIdx.x == 0)
-                    *prefix.n_items = run;
+                    *prefix.n_items = min(run, prefix.max_own);
         }
     }
     // TMA copies and the tensor core take over the space that these sums were in
@@ -641,6 +641,8 @@ latent_mma_kernel(const AttnParams p, const MmaPlan plan, const Prefix<SHARED> p
                 // (SHARED: of the pairs (item, block) in the order of the units, each has at least one number of the two one higher)
                 const int64_t slot = SHARED ? (int64_t)w.index + c : 2 * (int64_t)c + (w.t0 == 0 ? 1 : 0);
                 if constexpr (SHARED) {
+                    if (w.index >= prefix.max_own)  // (there is room for every item of tokens that are each one request's)
+                        continue;
                     if (tid == 0 && w.t0 == 0) {
                         const int2 own = own_of(prefix, w.r);
                         const int parts = w.nt == 0 ? 0 : holder(unit - 1 + (w.nt - w.t1), total, g) - c + 1;

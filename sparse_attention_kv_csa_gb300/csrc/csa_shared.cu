@@ -21,9 +21,9 @@
 // KB), eight to a ring.  S, P and O of neighbouring tiles overlap: S runs up to two tiles ahead, P has two buffers.  The running
 // reference m is raised only when a logit exceeds it by 2^8, so O is rarely touched outside the tensor core, and P stays below 2^8.
 //
-// 32768 query rows over 8192 rows of 512 columns (512 requests of 64 heads): 322 us, 1.71 PFLOP/s; what it took: two warps that
-// issue MMAs (482 us with one that waited for every unit), eight of exponentials, four that copy, arrivals that order no
-// global memory.
+// 32768 query rows over 8192 rows of 512 columns (512 requests of 64 heads): some 300 us, 1.8 PFLOP/s, 2500 cycles a tile of which the
+// tensor core needs 2048 (482 us with one warp that issued MMAs and waited for every unit, four of
+// exponentials, one that copied, and arrivals that ordered global memory too).
 //
 // Work is cut evenly over the pairs as in csa_latent_cuts.h.  Rows that are not bf16 in pages of whole groups of eight are first
 // widened to bf16 (8-bit values exactly; their scales stay apart) into an image of the prefix.
@@ -879,6 +879,7 @@ cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, con
     s.n_groups = n_groups;
     s.max_items = (int)(p.n_tokens * p.n_heads / kPairRows) + n_groups;
     s.image_rows = image_rows(p, n_groups);
+    s.max_own = own_items(p);
     const size_t slots = (size_t)s.max_items + s.clusters;
     const size_t own_slots = latent_behind_slots(p, num_sms);
     auto lay_out = [&](void *at) {
@@ -891,7 +892,7 @@ cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, con
         s.image_scales = w.take<float>(p.cache_dtype == CSA_DTYPE_E4M3 ? (size_t)n_groups * s.image_rows : 0);
         s.part_o = w.take<float>(slots * kPairRows * p.v_dim);
         s.part_ml = w.take<float2>(slots * kPairRows);
-        s.items = w.take<OwnItem>(own_items(p));
+        s.items = w.take<OwnItem>(s.max_own);
         s.n_items = w.take<int>(1);
         s.own_o = w.take<float>(own_slots * kOwnRows * p.v_dim);
         s.own_ml = w.take<float2>(own_slots * kOwnRows);
@@ -921,9 +922,8 @@ cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, con
     if (e == cudaSuccess)
         e = launch_latent_behind(p, s, num_sms, status, st);
     if (e == cudaSuccess) {
-        const int items = own_items(p);
-        const bool many = items > num_sms;
-        cfg.gridDim = dim3(items, many ? kOwnRows / 16 : kOwnRows * (p.v_dim / 128) / 8);
+        const bool many = s.max_own > num_sms;
+        cfg.gridDim = dim3(s.max_own, many ? kOwnRows / 16 : kOwnRows * (p.v_dim / 128) / 8);
         e = cudaLaunchKernelEx(&cfg, many ? shared_join_kernel<true> : shared_join_kernel<false>, p, (const SharedPlan)s);
     }
     const cudaError_t e2 = cudaFreeAsync(workspace, st);

@@ -46,10 +46,11 @@ struct SharedPlan {
     float *image_scales;  // [n_groups][image_rows], 8-bit rows only
     float *part_o;        // [max_items + clusters][128][v_dim]
     float2 *part_ml;      // [max_items + clusters][128]  (m, l)
-    OwnItem *items;       // [own_items()]
+    int max_own;          // own_items()
+    OwnItem *items;       // [max_own]
     int *n_items;
-    float *own_o;         // [own_items() + blocks][64][v_dim]
-    float2 *own_ml;       // [own_items() + blocks][64]
+    float *own_o;         // [max_own + blocks][64][v_dim]
+    float2 *own_ml;       // [max_own + blocks][64]
 };
 
 // The most items of 64 query rows.
