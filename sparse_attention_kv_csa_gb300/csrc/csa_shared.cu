@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(256) shared_image_kernel(const AttnParams p, c
 }
 
 // Joins the parts of the items' own rows and of their prefixes, in order.  Bound by a chain of five dependent reads, so where there
-// are many rows a warp has two of them, whole (64 requests' 8192 rows: 30.3 us with a warp for 128 columns of one row, 23.6 so, from cold caches), and
+// are many rows a warp has two of them, whole (128 requests' 8192 rows: 30.3 us with a warp for 128 columns of one row, 23.6 so, from cold caches), and
 // where there are few, whose parts may be many, 128 columns of one.
 struct JoinRow {
     int64_t prefix, own;  // rows of the prefix's parts and of its own ones
@@ -859,10 +859,12 @@ bool shared_mma_supported(const AttnParams &p, int n_groups, int num_sms)
         return false;
     // By requests an SM does a tile of 64 query rows x 64 rows in some 1 us, here the prefix's in 0.6, behind some 25 us of launches, parts
     // and their join.  Measured, in such tiles an SM by the table's width: 24 of 576 columns 59.5 us here, 54.8 by requests; another
-    // 24 45.8 and 49.6; 30 of 256 columns 38.5 and 39.6; with an image 31: 77.9 and 54.0, 70: 121 and 123.
+    // 24 45.8 and 49.6; 30 of 256 columns 38.5 and 39.6; of 128 and 192 columns, two blocks an SM by requests, 24: 43.5 and 35.4, 39: 55.3
+    // and 49.7, 54: 54.1 and 41.1, 58: 36.8 and 50.8, 103: 64.5 and 100.2; with four requests a
+    // group 48: 64.5 and 50.3; with an image 31: 77.9 and 54.0, 70: 121 and 123.
     const int64_t rows = p.n_tokens * p.n_heads / kOwnRows, items = rows > p.n_req ? rows : p.n_req;
     const int64_t tiles = ((int64_t)p.width * p.page_size + 63) / 64;
-    if (items * tiles < (needs_image(p) ? 64 : 24) * (int64_t)num_sms)
+    if (items * tiles < (needs_image(p) || p.head_dim <= 192 || p.n_req < 8 * n_groups ? 64 : 24) * (int64_t)num_sms)
         return false;
     // (the parts of a prompt's many tokens would take too much room: they fill the machine request by request)
     return ((p.n_tokens * p.n_heads / kPairRows + n_groups) * kPairRows + (int64_t)own_items(p) * kOwnRows) * p.v_dim * 4 <= (int64_t)1 << 32;
