@@ -65,6 +65,24 @@ CSA_BOTH int holder(long long unit, long long total, int g)
     return total < (1 << 20) ? (int)(((uint32_t)(unit + 1) * (uint32_t)g - 1) / (uint32_t)total) : (int)(((unit + 1) * g - 1) / total);
 }
 
+// The rings of a shared prefix's K and V, in units: shares of `slots` that go as the units of a tile, `least` each at least.
+struct PairRings {
+    int k, v;
+};
+
+CSA_BOTH PairRings pair_rings(int slots, int k_units, int v_units, int least)
+{
+    const int k = (slots * k_units + (k_units + v_units) / 2) / (k_units + v_units);
+    PairRings r;
+    r.k = k < least ? least : k > slots - least ? slots - least : k;
+    r.v = slots - r.k;
+    return r;
+}
+
+// Which of the two warps that fill a ring has a slot: always the same one, whether the ring has an even or an odd number of them.  A
+// barrier's parity tells a phase that is over from one that has not begun only to who took the one before.
+CSA_BOTH int ring_filler(int slot) { return slot & 1; }
+
 // What a block does of an item of nt tiles, from its unit `off` on with `left` units to do: `take` units, of them tiles
 // [t0, t1).  some: the item falls to this block too, by a tile or, without tiles, by its first unit.
 struct Segment {

@@ -458,7 +458,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
         }
     } else if (warp < kQueryWarp) {
         // ------------------------------------------------ rows by TMA, counted on the even block's barriers
-        // (two warps in turn for K, two for V: one took some 450 cycles a unit, with eight units a tile of 2048 cycles)
+        // (two warps for K, two for V, each with slots of its own: one took some 450 cycles a unit, with eight units a tile of 2048 cycles)
         const bool values = warp >= kCopyWarp + kCopyWarps / 2;
         const int base = values ? plan.k_slots : 0, slots = values ? plan.v_slots : plan.k_slots;
         const uint32_t kv_smem = smem_addr(kv_mem), full0 = at_rank(smem_addr(&sh.kv_full[0]), 0);
@@ -467,7 +467,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
         const int copies = 8 / plan.box_groups;
         int slot = base, filled = 0, last_filled = -1;
         uint32_t ph = 0;
-        bool turn = (warp - kCopyWarp) % 2 == 0;
+        const int filler = (warp - kCopyWarp) % 2;
         PairWalk w(s, sh, units);
         while (ok && w.next()) {
             const int32_t *table = p.block_table + (int64_t)w.q.first * p.table_stride;
@@ -484,7 +484,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
             };
             // 64 rows from group `first` of the tile on, chunks from `chunk` on
             auto fill = [&](int at, bool whole, int first, int chunk) {
-                if (turn && ok) {
+                if (ring_filler(slot - base) == filler && ok) {
                     const int g = __shfl_sync(~0u, at, first + (whole ? lane * plan.box_groups : lane) % 8);
                     if (filled >= slots) {
                         ok = mbar_wait(smem_addr(&sh.kv_empty[slot]), ph ^ 1, status);
@@ -500,7 +500,6 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                         last_filled = filled;
                     }
                 }
-                turn = !turn;
                 ++filled;
                 if (++slot == base + slots) {
                     slot = base;
@@ -524,8 +523,9 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
         }
         // no copy outlives the blocks, after a wait that gave up either (the even block's barriers count both blocks' copies)
         if (rank == 0 && lane == 0 && !ok)
-            for (int k = last_filled; k >= 0 && k > last_filled - slots; k -= 2)
-                mbar_wait(smem_addr(&sh.kv_full[base + k % slots]), (k / slots) & 1, status);
+            for (int k = last_filled; k >= 0 && k > last_filled - slots; --k)
+                if (ring_filler(k % slots) == filler)
+                    mbar_wait(smem_addr(&sh.kv_full[base + k % slots]), (k / slots) & 1, status);
         __syncwarp();
     } else {
         // ------------------------------------------------ queries, by copies of sixteen bytes
@@ -770,10 +770,9 @@ PairPlan make_plan(const AttnParams &p)
     const size_t limit = 227 * 1024 - sizeof(PairShared);
     // the rings' sizes go as the units of a tile, and are two or more: an MMA warp waits for two units at once
     const int fit = (int)((limit - fixed) / unit), slots = fit > kMaxSlots ? kMaxSlots : fit;
-    const int k_units = (m.nk + m.cw - 1) / m.cw, v_units = 2 * ((m.vch + m.cw - 1) / m.cw);
-    const int k_slots = (slots * k_units + (k_units + v_units) / 2) / (k_units + v_units);
-    m.k_slots = k_slots < kBatch ? kBatch : k_slots > slots - kBatch ? slots - kBatch : k_slots;
-    m.v_slots = slots - m.k_slots;
+    const PairRings rings = pair_rings(slots, (m.nk + m.cw - 1) / m.cw, 2 * ((m.vch + m.cw - 1) / m.cw), kBatch);
+    m.k_slots = rings.k;
+    m.v_slots = rings.v;
     m.smem = fixed + slots * unit;
     // a block an SM, beside none of the attention by requests (90 KB or more), which has tensor memory too
     m.smem = m.smem < 140 * 1024 ? 140 * 1024 : m.smem;
