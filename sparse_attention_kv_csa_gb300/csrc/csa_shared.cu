@@ -352,6 +352,8 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
             auto behind = [&](Place a) { return a.slot + 1 == base + slots ? Place{base, a.ph ^ 1} : Place{a.slot + 1, a.ph}; };
             auto ready = [&](Place a) { return mbar_test(smem_addr(&sh.kv_full[a.slot]), a.ph); };
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait(smem_addr(bar), parity, status)); };
+            // (for what threads of the other block have arrived at)
+            auto wait_both = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait_cluster(smem_addr(bar), parity, status)); };
             Place at{base, 0};
             int tile = 0;
             // the next units, all there or the wait gave up
@@ -377,10 +379,10 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                 int segment = 0;
                 while (ok && __shfl_sync(~0u, (int)w.next(), 0)) {
                     const int n = __shfl_sync(~0u, w.t1 - w.t0, 0);
-                    wait(&sh.q_full, segment++ & 1);
+                    wait_both(&sh.q_full, segment++ & 1);
                     for (int j = 0; ok && j < n; ++j, ++tile) {  // S = Q K^T
                         if (tile > 1)
-                            wait(&sh.p_full[tile & 1], (tile - 2) >> 1 & 1);  // S of two tiles before has been read
+                            wait_both(&sh.p_full[tile & 1], (tile - 2) >> 1 & 1);  // S of two tiles before has been read
                         const uint32_t d = tm + 256 + (tile & 1) * 64;
                         for (int first = 0; ok && first < nk; first += kBatch * cw) {
                             const int count = min(kBatch, (nk - first + cw - 1) / cw);
@@ -423,7 +425,7 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                             if (!arrived(u, count))
                                 break;
                             if (first == 0) {
-                                wait(&sh.p_full[tile & 1], tile >> 1 & 1);
+                                wait_both(&sh.p_full[tile & 1], tile >> 1 & 1);
                                 if (!ok)
                                     break;
                                 tc_fence_after();

@@ -154,12 +154,44 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
-// An arrival at a barrier of either block.  What it orders are reads of tensor memory (behind tcgen05.fence) and writes to this
-// block's own shared memory (behind fence.proxy.async), for the products that read them here: nothing of global memory, for which
-// a release at the cluster's scope takes some 2000 cycles (and an acquire some 100 in the warps that issue the products).
+// An arrival at a barrier of either block, and the wait of a thread that issues products for both.  Between them they order, at the
+// cluster's scope, the arriving warps' reads of tensor memory (behind tcgen05.fence) and writes to their own block's shared memory (behind
+// fence.proxy.async) before the products that overwrite and read them.  The fences are held to shared memory: a release of global
+// memory at that scope takes some 2000 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+        : "memory");
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned *status)
+{
+    auto done = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    bool over = done();
+    if (!over) {
+        const uint64_t t0 = global_ns();
+        for (uint32_t it = 1; it < (1u << 28) && !over; ++it) {
+            over = done();
+            if ((it & 255u) == 0 && global_ns() - t0 > kWaitLimitNs)
+                break;
+        }
+        if (!over)
+            atomicCAS(status, 0u, kStatusTimeout);
+    }
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+    return over;
 }
 
 // (a warp of each block)
