@@ -197,7 +197,8 @@ CSA_API int csa_latent_attention(const void *q, int64_t q_token_stride, int64_t 
  * shared_rows int32 [n_groups].  Rows that some token of the group does not see are not shared, whatever shared_rows says.
  * What is read once is whole pages of the first request of a group that has new tokens, up to its first table entry outside the
  * cache; none in a group with a request of more rows than its table lists.  Rows of 128 to 576 columns in multiples of 64 with
- * v_dim 128, 256, 384 or 512 are shared, in calls large enough to gain from it; others are read by request.
+ * v_dim 128, 256, 384 or 512 are shared, in calls large enough to gain from it; others are read by request, as is a call for
+ * whose parts (fp32 sums of every query row, 4 GiB at most) the device has no memory.
  * Everything else, and every limit, as in csa_latent_attention; n_groups <= 14000.
  */
 CSA_API int csa_shared_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q,

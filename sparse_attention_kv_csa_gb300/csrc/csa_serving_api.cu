@@ -341,6 +341,10 @@ int csa_shared_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     if (!csa::shared_mma_supported(p, n_groups, sms))
         return run_attention(p, stream);
     e = csa::launch_shared_mma(p, cu_groups, shared_rows, n_groups, sms, pool, status, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorMemoryAllocation) {  // no room for the parts: by request a call needs a few MB, and gives the same
+        cudaGetLastError();                // (nor does the next caller of CUDA meet that error)
+        return run_attention(p, stream);
+    }
     return e == cudaSuccess ? CSA_OK : cuda_status(e, "shared attention launch");
 }
 
