@@ -4,7 +4,7 @@
 
 namespace csa {
 
-int latent_behind_slots(const AttnParams &p, int num_sms) { return own_items(p) + make_plan(p, num_sms).blocks; }
+int latent_behind_slots(const AttnParams &p, int num_sms) { return (int)own_items(prefix_call(p, 0)) + make_plan(p, num_sms).blocks; }
 
 cudaError_t launch_latent_behind(const AttnParams &p, const SharedPlan &s, int num_sms, unsigned *status, cudaStream_t st)
 {

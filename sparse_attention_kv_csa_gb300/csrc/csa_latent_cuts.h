@@ -13,6 +13,11 @@
 
 namespace csa {
 
+#ifndef __CUDA_ARCH__
+using std::max;
+using std::min;
+#endif
+
 // n / d for 0 <= n < 2^31 by a multiplication (T. Granlund and P. Montgomery, "Division by invariant integers using
 // multiplication", PLDI 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (hi(m n) + n) >> l.
 struct Divider {
@@ -44,11 +49,6 @@ constexpr int kMinUnits = 3;
 
 // The same for an item of a shared prefix.
 constexpr int kPairHead = 2;
-
-#ifndef __CUDA_ARCH__
-using std::max;
-using std::min;
-#endif
 
 // How many blocks share the units.
 CSA_BOTH int sharing(long long total, int blocks) { return (int)max(1ll, min(total / kMinUnits, (long long)blocks)); }
@@ -82,6 +82,57 @@ CSA_BOTH PairRings pair_rings(int slots, int k_units, int v_units, int least)
 // Which of the two warps that fill a ring has a slot: always the same one, whether the ring has an even or an odd number of them.  A
 // barrier's parity tells a phase that is over from one that has not begun only to who took the one before.
 CSA_BOTH int ring_filler(int slot) { return slot & 1; }
+
+// What the choice of a way through a call with shared prefixes goes by: all of it is known to the host.
+struct PrefixCall {
+    long long n_tokens;
+    int n_heads, n_req, n_groups, head_dim, v_dim;
+    bool bits8;
+    long long n_pages;
+    int page_size, width;
+};
+
+constexpr int kPairRows = 128;  // query rows of an item of a shared prefix, and cache rows of its tiles
+constexpr int kOwnRows = 64;    // query rows of an item of the rows behind it
+
+// Widths that the attentions' tensor-core kernels take.
+CSA_BOTH bool on_tensor_cores(int head_dim, int v_dim) { return head_dim % 64 == 0 && head_dim <= 576 && v_dim % 64 == 0 && v_dim <= 512; }
+
+// The most items of rows behind prefixes.
+CSA_BOTH long long own_items(const PrefixCall &c) { return c.n_tokens * c.n_heads / kOwnRows + c.n_req; }
+
+// Rows that TMA does not bring as bf16 in whole groups of eight are copied once into an image of the prefix.
+CSA_BOTH bool needs_image(const PrefixCall &c) { return c.bits8 || c.page_size % 8 != 0; }
+
+// Rows of a group's image: as many as a table lists and the cache has (a table may have room for far more), within a GiB for all groups.
+// Rows of a prefix past them are read by request.
+CSA_BOTH int image_rows(const PrefixCall &c)
+{
+    if (!needs_image(c))
+        return 0;
+    const long long room = (1ll << 30) / ((long long)c.n_groups * c.head_dim * 2) / kPairRows * kPairRows;
+    const long long pages = min((long long)c.width, c.n_pages);
+    return (int)min(room, (pages * c.page_size + kPairRows - 1) / kPairRows * kPairRows);
+}
+
+// Whether prefixes are read apart.  By requests an SM does a tile of 64 query rows x 64 rows in some 1 us, here the prefix's in 0.6, behind
+// some 25 us of launches, parts and their join.  Measured, in such tiles an SM by the table's width: 24 of 576 columns 59.5 us
+// here, 54.8 by requests; another 24 45.8 and 49.6; 30 of 256 columns 38.5 and 39.6; of 128 and 192 columns, two blocks an SM by
+// requests, 24: 43.5 and 35.4, 39: 55.3 and 49.7, 54: 54.1 and 41.1, 58: 36.8 and 50.8, 103: 64.5 and 100.2, 275: 128.1 and 117.6; with
+// four requests a group 48: 64.5 and 50.3; with an image 31: 77.9 and 54.0, 70: 121 and 123.  So the rule is a rough one (the two at
+// 58 and 275 go the other way), and a table wider than its requests need counts as if it were full.
+CSA_BOTH bool prefix_apart(const PrefixCall &c, int num_sms)
+{
+    if (!on_tensor_cores(c.head_dim, c.v_dim) || c.v_dim % 128 != 0 || c.n_groups < 1 || c.n_req < 2 ||
+        (long long)c.width * c.page_size < kPairRows || (needs_image(c) && image_rows(c) < kPairRows))
+        return false;
+    const long long rows = c.n_tokens * c.n_heads / kOwnRows, items = max(rows, (long long)c.n_req);
+    const long long tiles = ((long long)c.width * c.page_size + 63) / 64;
+    if (items * tiles < (needs_image(c) || c.head_dim <= 192 || c.n_req < 8 * c.n_groups ? 64 : 24) * (long long)num_sms)
+        return false;
+    // (the parts of a prompt's many tokens would take too much room: they fill the machine request by request)
+    return ((c.n_tokens * c.n_heads / kPairRows + c.n_groups) * kPairRows + own_items(c) * kOwnRows) * c.v_dim * 4 <= 1ll << 32;
+}
 
 // What a block does of an item of nt tiles, from its unit `off` on with `left` units to do: `take` units, of them tiles
 // [t0, t1).  some: the item falls to this block too, by a tile or, without tiles, by its first unit.

@@ -1194,7 +1194,7 @@ cudaError_t launch_mma(const AttnParams &p, const Prefix<SHARED> &prefix, void *
 #ifndef CSA_BEHIND_PREFIX
 bool latent_mma_supported(const AttnParams &p)
 {
-    return p.head_dim % 64 == 0 && p.head_dim <= 576 && p.v_dim % 64 == 0 && p.v_dim <= 512;
+    return on_tensor_cores(p.head_dim, p.v_dim);
 }
 
 size_t latent_mma_workspace(const AttnParams &p, int num_sms)

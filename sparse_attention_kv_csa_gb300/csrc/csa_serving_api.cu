@@ -338,7 +338,7 @@ int csa_shared_attention(const void *q, int64_t q_token_stride, int64_t q_head_s
     cudaError_t e = csa::device_facts(&sms, &pool, &status);
     if (e != cudaSuccess)
         return cuda_status(e, "device set-up");
-    if (!csa::shared_mma_supported(p, n_groups, sms))
+    if (!csa::prefix_apart(csa::prefix_call(p, n_groups), sms))
         return run_attention(p, stream);
     e = csa::launch_shared_mma(p, cu_groups, shared_rows, n_groups, sms, pool, status, static_cast<cudaStream_t>(stream));
     if (e == cudaErrorMemoryAllocation) {  // no room for the parts: by request a call needs a few MB, and gives the same

@@ -150,12 +150,16 @@ struct AttnParams {
     float *lse;
     Divider by_heads, by_ratio, by_page;
 };
+inline PrefixCall prefix_call(const AttnParams &p, int n_groups)
+{
+    return PrefixCall{p.n_tokens, p.n_heads, p.n_req, n_groups, p.head_dim, p.v_dim, p.cache_dtype == CSA_DTYPE_E4M3, p.n_pages, p.page_size, p.width};
+}
 // Tensor-core kernel: widths in multiples of 64 up to 576 and 512; the workspace holds the parts of split items.
 bool latent_mma_supported(const AttnParams &p);
 size_t latent_mma_workspace(const AttnParams &p, int num_sms);
 cudaError_t launch_latent_mma(const AttnParams &p, void *workspace, int num_sms, unsigned *status, cudaStream_t st);
-// The same for groups of requests that share a prefix (csa_shared.cu); takes its workspace from the pool itself.
-bool shared_mma_supported(const AttnParams &p, int n_groups, int num_sms);
+// The same for groups of requests that share a prefix (csa_shared.cu), where prefix_apart() says so; takes its workspace from the pool
+// itself.
 cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, const int32_t *shared_rows, int n_groups, int num_sms,
                               cudaMemPool_t pool, unsigned *status, cudaStream_t st);
 struct SharedPlan;

@@ -47,7 +47,6 @@ constexpr int kBatch = 2;  // units that an MMA warp waits for at once
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;  // log2 of how far a logit may exceed the reference
-constexpr int kLeastShared = kPairRows;  // rows of a prefix at least
 
 struct PairPlan {
     int nk;           // chunks of 64 columns of a row
@@ -760,8 +759,6 @@ template <bool MANY> __global__ void __launch_bounds__(256) shared_join_kernel(c
     }
 }
 
-bool needs_image(const AttnParams &p) { return p.cache_dtype == CSA_DTYPE_E4M3 || p.page_size % 8 != 0; }
-
 PairPlan make_plan(const AttnParams &p)
 {
     PairPlan m{};
@@ -778,7 +775,7 @@ PairPlan make_plan(const AttnParams &p)
     m.smem = fixed + slots * unit;
     // a block an SM, beside none of the attention by requests (90 KB or more), which has tensor memory too
     m.smem = m.smem < 140 * 1024 ? 140 * 1024 : m.smem;
-    const int groups = needs_image(p) ? 8 : p.page_size / 8;
+    const int groups = needs_image(prefix_call(p, 0)) ? 8 : p.page_size / 8;
     for (m.box_groups = 8; groups % m.box_groups; m.box_groups /= 2) {}
     return m;
 }
@@ -812,16 +809,6 @@ cudaError_t launch_pair(const AttnParams &p, const SharedPlan &s, const PairPlan
     return cudaLaunchKernelEx(&cfg, kern, p, s, m, boxes, groups, status);
 }
 
-// Rows of a group's image, within a GiB for all groups.
-int image_rows(const AttnParams &p, int n_groups)
-{
-    if (!needs_image(p))
-        return 0;
-    const int64_t room = ((int64_t)1 << 30) / ((int64_t)n_groups * p.head_dim * 2) / kPairRows * kPairRows;
-    const int64_t most = ((int64_t)p.width * p.page_size + kPairRows - 1) / kPairRows * kPairRows;
-    return (int)(room < most ? room : most);
-}
-
 template <bool BITS8>
 cudaError_t launch_pair(const AttnParams &p, const SharedPlan &s, const PairPlan &m, unsigned *status, cudaStream_t st)
 {
@@ -852,37 +839,19 @@ struct Pieces {
 
 }  // namespace
 
-int own_items(const AttnParams &p) { return (int)(p.n_tokens * p.n_heads / kOwnRows) + p.n_req; }
-
-bool shared_mma_supported(const AttnParams &p, int n_groups, int num_sms)
-{
-    if (!latent_mma_supported(p) || p.v_dim % 128 != 0 || n_groups < 1 || p.n_req < 2 || p.width * p.page_size < kLeastShared || (needs_image(p) && image_rows(p, n_groups) < kPairRows))
-        return false;
-    // By requests an SM does a tile of 64 query rows x 64 rows in some 1 us, here the prefix's in 0.6, behind some 25 us of launches, parts
-    // and their join.  Measured, in such tiles an SM by the table's width: 24 of 576 columns 59.5 us here, 54.8 by requests; another
-    // 24 45.8 and 49.6; 30 of 256 columns 38.5 and 39.6; of 128 and 192 columns, two blocks an SM by requests, 24: 43.5 and 35.4, 39: 55.3
-    // and 49.7, 54: 54.1 and 41.1, 58: 36.8 and 50.8, 103: 64.5 and 100.2; with four requests a
-    // group 48: 64.5 and 50.3; with an image 31: 77.9 and 54.0, 70: 121 and 123.
-    const int64_t rows = p.n_tokens * p.n_heads / kOwnRows, items = rows > p.n_req ? rows : p.n_req;
-    const int64_t tiles = ((int64_t)p.width * p.page_size + 63) / 64;
-    if (items * tiles < (needs_image(p) || p.head_dim <= 192 || p.n_req < 8 * n_groups ? 64 : 24) * (int64_t)num_sms)
-        return false;
-    // (the parts of a prompt's many tokens would take too much room: they fill the machine request by request)
-    return ((p.n_tokens * p.n_heads / kPairRows + n_groups) * kPairRows + (int64_t)own_items(p) * kOwnRows) * p.v_dim * 4 <= (int64_t)1 << 32;
-}
-
 cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, const int32_t *shared_rows, int n_groups, int num_sms,
                               cudaMemPool_t pool, unsigned *status, cudaStream_t st)
 {
     const PairPlan m = make_plan(p);
+    const PrefixCall call = prefix_call(p, n_groups);
     SharedPlan s{};
     cudaError_t e = clusters_of(p, m, &s.clusters);
     if (e != cudaSuccess)
         return e;
     s.n_groups = n_groups;
     s.max_items = (int)(p.n_tokens * p.n_heads / kPairRows) + n_groups;
-    s.image_rows = image_rows(p, n_groups);
-    s.max_own = own_items(p);
+    s.image_rows = image_rows(call);
+    s.max_own = (int)own_items(call);
     const size_t slots = (size_t)s.max_items + s.clusters;
     const size_t own_slots = latent_behind_slots(p, num_sms);
     auto lay_out = [&](void *at) {
@@ -914,7 +883,7 @@ cudaError_t launch_shared_mma(const AttnParams &p, const int32_t *cu_groups, con
     cfg.stream = st;
     cfg.blockDim = dim3(256);
     cfg.gridDim = dim3(n_groups);
-    e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, cu_groups, shared_rows, kLeastShared, (const SharedPlan)s);
+    e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, p, cu_groups, shared_rows, kPairRows, (const SharedPlan)s);
     if (e == cudaSuccess && s.image_rows > 0) {
         const int most = (s.image_rows + 7) / 8, each = (8 * num_sms + n_groups - 1) / n_groups;
         cfg.gridDim = dim3(most < each ? most : each, n_groups);

@@ -11,8 +11,6 @@
 
 namespace csa {
 
-constexpr int kPairRows = 128;  // query rows of an item, and cache rows of a tile
-
 struct GroupInfo {
     int shared;  // rows that the group's prefix part takes: whole pages, seen by every new token of the group
     int tiles;
@@ -27,7 +25,6 @@ struct GroupSums {
 };
 
 // An item of 64 query rows of one request, and the parts of its own rows.
-constexpr int kOwnRows = 64;
 struct OwnItem {
     int row, rows;
     int group;        // whose prefix its rows see besides (-1: none)
@@ -52,10 +49,6 @@ struct SharedPlan {
     float *own_o;         // [max_own + blocks][64][v_dim]
     float2 *own_ml;       // [max_own + blocks][64]
 };
-
-// The most items of 64 query rows.
-struct AttnParams;
-int own_items(const AttnParams &p);
 
 #ifdef __CUDACC__
 // What a part's sums count for beside a reference of m.

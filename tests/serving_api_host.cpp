@@ -63,7 +63,6 @@ cudaError_t device_facts(int *sms, cudaMemPool_t *pool, unsigned **status)
 bool latent_mma_supported(const AttnParams &) { return true; }
 size_t latent_mma_workspace(const AttnParams &, int) { return 64; }
 cudaError_t launch_latent_mma(const AttnParams &, void *, int, unsigned *, cudaStream_t) { return ++g.latent, cudaSuccess; }
-bool shared_mma_supported(const AttnParams &, int, int) { return true; }
 cudaError_t launch_shared_mma(const AttnParams &, const int32_t *, const int32_t *, int, int, cudaMemPool_t, unsigned *, cudaStream_t)
 {
     g.last = g.shared_result;

@@ -29,7 +29,8 @@ def shared(api, shared_result=0, malloc_result=0):
     """The status of one call, and how often what was called."""
     a = 4096  # (an address that nothing reads)
     api.fake_reset(shared_result, malloc_result)
-    rc = api.csa_shared_attention(a, 512, 512, a, 4, 4, 1, 512, 512, a, 512, 0, None, 100, 64, a, 9, 9, a, a, a, 1, 1, 1.0, None, a, None, None)
+    rc = api.csa_shared_attention(a, 64 * 512, 512, a, 64, 64, 64, 512, 512, a, 512, 0, None, 100, 64, a, 90, 90, a, a, a, 1, 1, 1.0, None, a, None,
+                                  None)
     n = (ctypes.c_int * 7)()
     api.fake_counts(n)
     return rc, dict(zip(("shared", "latent", "plain", "mallocs", "frees", "cleared", "last"), n))
