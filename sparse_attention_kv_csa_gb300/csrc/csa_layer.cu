@@ -11,7 +11,8 @@ layer_fwd_kernel(const LayerFwdParams p)
 {
     constexpr int kThreads = TEAM < 128 ? 128 : TEAM;
     constexpr int kTeams = kThreads / TEAM;
-    __shared__ float buf[4][kThreads / 32];
+    __shared__ float buf[2][kThreads / 32];
+    __shared__ float2 buf2[2][kThreads / 32];
     __shared__ uint64_t all_full[kTeams * kMaxRing];
     extern __shared__ __align__(128) uint8_t ring_mem[];
     const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
@@ -106,20 +107,22 @@ layer_fwd_kernel(const LayerFwdParams p)
                 refill(row + ring.stages * step, at.stage);
             ring.next(at);
         }
-        float2 ss = splat(0.0f);
+        float2 ss = splat(0.0f), rest = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (live && (i * TEAM + t) * VEC < p.dim) {
                 add_to(h[i], -mu);
                 ss = dot_add(h[i], h[i], ss);
+                rest = sum_add(h[i], rest);
             }
-        const float var = team_reduce<TEAM, false>(ss.x + ss.y, buf[2 + (it & 1)]) * inv_dim;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
+        const float2 second = mul2(team_sum2<TEAM>(make_float2(ss.x + ss.y, rest.x + rest.y), buf2[it & 1]), splat(inv_dim));
+        const float off = second.y, var = fmaf(-off, off, second.x);
+        const float rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + p.eps);  // (NaN stays)
         if (!live)
             continue;
         if (t == 0) {
             if (p.mean)
-                p.mean[row] = mu;
+                p.mean[row] = mu + off;
             if (p.rstd)
                 p.rstd[row] = rstd;
         }
@@ -127,7 +130,7 @@ layer_fwd_kernel(const LayerFwdParams p)
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TEAM + t) * VEC;
             if (c < p.dim) {
-                scale_by(h[i], rstd);
+                scale_add(h[i], rstd, -off * rstd);
                 fma_by(h[i], w[i], b[i]);
                 store<T, VEC>(static_cast<T *>(p.out) + row * p.out_stride + c, pack<T, VEC>(h[i]));
             }
