@@ -349,9 +349,8 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                 uint32_t ph;
             };
             auto behind = [&](Place a) { return a.slot + 1 == base + slots ? Place{base, a.ph ^ 1} : Place{a.slot + 1, a.ph}; };
-            auto ready = [&](Place a) { return mbar_test(smem_addr(&sh.kv_full[a.slot]), a.ph); };
-            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait(smem_addr(bar), parity, status)); };
-            // (for what threads of the other block have arrived at)
+            // (threads and copies of the other block arrive at all of these barriers)
+            auto ready = [&](Place a) { return mbar_test_cluster(smem_addr(&sh.kv_full[a.slot]), a.ph); };
             auto wait_both = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(~0u, ok && mbar_wait_cluster(smem_addr(bar), parity, status)); };
             Place at{base, 0};
             int tile = 0;
@@ -366,9 +365,11 @@ latent_pair_kernel(const AttnParams p, const SharedPlan s, const PairPlan plan, 
                         at = behind(at);
                     }
                 }
-                if (!__all_sync(~0u, here))
+                if (__all_sync(~0u, here))
+                    acquire_cluster();
+                else
                     for (int i = 0; i < count && ok; ++i)
-                        wait(&sh.kv_full[u[i].slot], u[i].ph);
+                        wait_both(&sh.kv_full[u[i].slot], u[i].ph);
                 tc_fence_after();
                 return ok;
             };

@@ -156,14 +156,30 @@ __device__ __forceinline__ void cluster_barrier()
 
 // An arrival at a barrier of either block, and the wait of a thread that issues products for both.  Between them they order, at the
 // cluster's scope, the arriving warps' reads of tensor memory (behind tcgen05.fence) and writes to their own block's shared memory (behind
-// fence.proxy.async) before the products that overwrite and read them.  The fences are held to shared memory: a release of global
-// memory at that scope takes some 2000 cycles.
+// fence.proxy.async), or the other block's copies, before the products that overwrite and read them.  The fences are held to shared
+// memory: a release of global memory at that scope takes some 2000 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile(
         "fence.release.sync_restrict::shared::cta.cluster;\n\t"
         "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
         : "memory");
+}
+
+__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
+
+// (acquire_cluster() makes what it saw an acquire)
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned *status)
@@ -190,7 +206,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
         if (!over)
             atomicCAS(status, 0u, kStatusTimeout);
     }
-    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+    acquire_cluster();
     return over;
 }
 

@@ -20,7 +20,8 @@ def test_arrivals_across_blocks_release_and_their_waits_acquire_at_the_clusters_
     """A block's queries and weights, written to its own shared memory, are read by products that the other block's threads issue: the
     arrival that says so has to release at the cluster's scope, a barrier operation of that scope carries it, and the wait acquires."""
     text = source("csa_tcgen05.cuh")
-    arrive, wait = body(text, "void mbar_arrive_cluster("), body(text, "bool mbar_wait_cluster(")
+    arrive, wait = body(text, "void mbar_arrive_cluster("), body(text, "bool mbar_wait_cluster(").replace(
+        "acquire_cluster();", "fence.acquire.cluster;" if "fence.acquire." in body(text, "void acquire_cluster()") else "")
     assert re.search(r"fence\.release\.[\w:.]*cluster;.*mbarrier\.arrive\.\w+\.cluster\.shared::cluster", arrive, re.S) or \
         "mbarrier.arrive.release.cluster" in arrive
     assert re.search(r"mbarrier\.try_wait\.parity\.\w+\.cluster", wait)
@@ -41,3 +42,11 @@ def test_the_warps_of_products_wait_so_for_both_blocks_arrivals():
             before = kernel[:at]
             assert before.rindex("fence_async_smem();") > max(before.rindex("copy_async_16(") if bar == "q_full" else before.rindex("make_uint4("), 0)
         assert "mbar_arrive_cluster(%s" % bar in kernel
+
+
+def test_and_for_the_other_blocks_copies():
+    kernel = source("csa_shared.cu")
+    issue = kernel[kernel.index("kQueryStep = kQueryChunk"):kernel.index("mma_commit_pair(smem_addr(&sh.drained))")]
+    here = issue[issue.index("auto arrived ="):issue.index("PairWalk w(")]
+    assert "mbar_test_cluster(" in issue[issue.index("auto ready ="):issue.index("auto arrived =")]
+    assert "acquire_cluster();" in here and "wait_both(&sh.kv_full[" in here and " wait(" not in issue
