@@ -40,7 +40,7 @@ def test_a_prefix_that_lists_pages_twice(page, bits8):
     # its image has room for the cache's rows once; those behind are read by request
     a = shared.made([(300, [(40, 1), (9, 2), (0, 1)])], 32, 512, 1, page, bits8, True, seed=24)
     whole = 300 // page
-    wide = torch.full((3, 4000), -1, dtype=torch.int32, device="cuda")
+    wide = torch.full((3, 5000), -1, dtype=torch.int32, device="cuda")
     for k in range(5):
         wide[:, k * whole:(k + 1) * whole] = a["block_table"][:, :whole]
     wide[:, 5 * whole:5 * whole + 3] = a["block_table"][:, whole:whole + 3]
