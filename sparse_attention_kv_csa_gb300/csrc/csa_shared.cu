@@ -18,10 +18,10 @@
 //   O += P V           128 x v_dim: each block loads half of the value columns of all 128 rows
 //
 // so a block loads 128 KB for the 33.6 MFLOP of the two at 512 columns, in units of 64 rows x up to two chunks of 64 columns (16
-// KB), eight to a ring.  S, P and O of neighbouring tiles overlap: S runs up to two tiles ahead, P has two buffers.  The running
+// KB), through a ring for K and one for V (four units each there; seven in all for rows of 576).  S, P and O of neighbouring tiles overlap: S runs up to two tiles ahead, P has two buffers.  The running
 // reference m is raised only when a logit exceeds it by 2^8, so O is rarely touched outside the tensor core, and P stays below 2^8.
 //
-// 32768 query rows over 8192 rows of 512 columns (512 requests of 64 heads): some 300 us, 1.8 PFLOP/s, 2500 cycles a tile of which the
+// 32768 query rows over 8192 rows of 512 columns (512 requests of 64 heads): some 300 us of the call's 411, 1.8 PFLOP/s, 2500 cycles a tile of which the
 // tensor core needs 2048 (482 us with one warp that issued MMAs and waited for every unit, four of
 // exponentials, one that copied, and arrivals that ordered global memory too).
 //
